@@ -12,6 +12,11 @@ Functions mirror the C ABI names: ``pack_bits``, ``pack``, ``unpack``,
 ``status_str``.  Weight descriptors are built with ``Lut6Weights``,
 ``FabqWeights`` and ``MdbfWeights``; their ``from_*`` constructors upload
 unpacked host arrays and pack them on the GPU with ``fqm_pack_bits``.
+
+Around the products: ``add_rms_norm`` (the residual's addition and the norm in
+front of a product, with an 8-bit form), ``Adapters`` and ``lora`` (low-rank
+adapters of many requests beside a product) and ``gemm_grouped`` (the products
+of many experts, ragged sizes).
 """
 from __future__ import annotations
 
@@ -26,18 +31,20 @@ LIB_PATH = os.path.join(HERE, "libfqm.so")
 
 FQM_LUT6, FQM_FABQ, FQM_MDBF, FQM_LUT4 = 1, 2, 3, 4
 FQM_CB_SCALAR16, FQM_CB_TIERED, FQM_CB_VECTOR = 0, 1, 2
-FQM_BF16, FQM_F32 = 0, 1
+FQM_BF16, FQM_F32, FQM_I8 = 0, 1, 2
 
 __all__ = [
     "FqmError", "FqmNotBuilt", "load", "version", "set_debug", "status_str", "pack_bits", "pack",
     "unpack", "dequant", "workspace_size", "gemv", "gemv_static", "gemm_workspace_size", "gemm", "Lut6Weights", "Lut4Weights", "FabqWeights",
-    "MdbfWeights", "SYMBOLS",
+    "MdbfWeights", "SYMBOLS", "add_rms_norm", "NormOut", "Adapters", "lora_workspace_size", "lora",
+    "gemm_grouped_workspace_size", "gemm_grouped",
 ]
 
 # Every symbol include/fqm.h declares.
 SYMBOLS = ("fqm_version", "fqm_set_debug", "fqm_status_str", "fqm_pack_bits", "fqm_pack", "fqm_unpack",
            "fqm_dequant", "fqm_workspace_size", "fqm_gemv", "fqm_gemv_static",
-           "fqm_gemm_workspace_size", "fqm_gemm")
+           "fqm_gemm_workspace_size", "fqm_gemm", "fqm_add_rms_norm", "fqm_lora_workspace_size", "fqm_lora",
+           "fqm_gemm_grouped_workspace_size", "fqm_gemm_grouped")
 STATIC_SCRATCH_BYTES = 16 << 20  # FQM_STATIC_SCRATCH_BYTES
 
 
@@ -88,6 +95,26 @@ class _Weights(ctypes.Structure):
                 ("fabq", _Fabq), ("mdbf", _Mdbf), ("lut4", _Lut4)]
 
 
+class _Norm(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("terms", c_int32), ("x_dtype", c_int32),
+                ("res_dtype", c_int32), ("weight_dtype", c_int32), ("y_dtype", c_int32), ("eps", ctypes.c_float),
+                ("x", c_void_p), ("ld_x", c_int64), ("ld_term", c_int64), ("residual", c_void_p),
+                ("ld_res", c_int64), ("weight", c_void_p), ("total", c_void_p), ("ld_total", c_int64),
+                ("y", c_void_p), ("ld_y", c_int64), ("y_scale", c_void_p)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("count", c_int32), ("rank", c_int32), ("rows", c_int64), ("cols", c_int64),
+                ("A", c_void_p), ("ld_A", c_int64), ("B", c_void_p), ("ld_B", c_int64),
+                ("scale", c_void_p), ("ranks", c_void_p)]
+
+
+class _Groups(ctypes.Structure):
+    _fields_ = [("count", c_int32), ("offsets", c_void_p), ("M", c_int64), ("X", c_void_p), ("x_dtype", c_int32),
+                ("x_rows", c_int64), ("x_scale", c_void_p), ("src", c_void_p), ("Y", c_void_p),
+                ("y_dtype", c_int32), ("y_rows", c_int64), ("dst", c_void_p), ("row_scale", c_void_p)]
+
+
 _lib = None
 
 
@@ -124,6 +151,17 @@ def load():
     lib.fqm_gemm.argtypes = [P(_Weights), c_void_p, c_void_p, c_int64, c_void_p, ctypes.c_size_t, c_void_p]
     lib.fqm_gemm_workspace_size.restype = ctypes.c_size_t
     lib.fqm_gemm_workspace_size.argtypes = [P(_Weights), c_int64]
+    lib.fqm_add_rms_norm.restype = c_int32
+    lib.fqm_add_rms_norm.argtypes = [P(_Norm), c_void_p]
+    lib.fqm_lora_workspace_size.restype = ctypes.c_size_t
+    lib.fqm_lora_workspace_size.argtypes = [P(_Adapters), c_int64]
+    lib.fqm_lora.restype = c_int32
+    lib.fqm_lora.argtypes = [P(_Adapters), c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int64,
+                             c_void_p, ctypes.c_size_t, c_void_p]
+    lib.fqm_gemm_grouped_workspace_size.restype = ctypes.c_size_t
+    lib.fqm_gemm_grouped_workspace_size.argtypes = [P(_Weights), P(_Groups)]
+    lib.fqm_gemm_grouped.restype = c_int32
+    lib.fqm_gemm_grouped.argtypes = [P(_Weights), P(_Groups), c_void_p, ctypes.c_size_t, c_void_p]
     _lib = lib
     return lib
 
@@ -538,3 +576,7 @@ def gemm(w: _WeightsBase, X: torch.Tensor, Y: torch.Tensor | None = None,
     _check(load().fqm_gemm(w.ref, _ptr(X), _ptr(Y), M, _ptr(workspace), ws_bytes, _stream(stream)),
            "fqm_gemm")
     return Y
+
+
+from ._layer import (Adapters, NormOut, add_rms_norm, gemm_grouped,  # noqa: E402
+                     gemm_grouped_workspace_size, lora, lora_workspace_size)

@@ -3,11 +3,12 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <mutex>
 
-#include "fqm_internal.h"
+#include "fqm_layer.h"
 
 using namespace fqm;
 
@@ -440,6 +441,179 @@ fqm_status fqm_gemm(const fqm_weights* w, const uint16_t* X, uint16_t* Y, int64_
     else
         r = hip_status(launch_lut_gemm(*w, X, Y, M, workspace, ws_bytes, s));
     return debug_finish(r, s);
+}
+
+}  // extern "C"
+
+// ---- the operators around the products ---------------------------------------
+
+namespace {
+
+inline bool value_dtype(int32_t t) { return t == FQM_BF16 || t == FQM_F32; }
+inline int64_t dtype_bytes(int32_t t) { return t == FQM_F32 ? 4 : t == FQM_BF16 ? 2 : 1; }
+inline bool aligned_to(const void* p, int64_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
+}
+// `rows` rows of `need` elements `ld` apart: the stride holds a row and the
+// extent in bytes stays far inside int64.
+inline bool rows_ok(int64_t rows, int64_t ld, int64_t need) {
+    return ld >= need && ld <= ((int64_t)1 << 40) && rows <= ((int64_t)1 << 58) / std::max<int64_t>(ld, 1);
+}
+
+fqm_status check_norm(const fqm_norm* a) {
+    if (!a) return FQM_E_NULL;
+    if (a->rows < 0 || a->rows > 0x7fffffff || a->cols < 0 || a->cols > 32768 || a->terms < 1 || a->terms > 64)
+        return FQM_E_SHAPE;
+    if (!value_dtype(a->x_dtype) || (a->residual && !value_dtype(a->res_dtype)) ||
+        (a->weight && !value_dtype(a->weight_dtype)) || !(value_dtype(a->y_dtype) || a->y_dtype == FQM_I8) ||
+        !(a->eps >= 0.f && a->eps <= 3.4e38f))
+        return FQM_E_FORMAT;
+    if (a->rows == 0) return FQM_OK;
+    if (a->y_dtype == FQM_I8 && !a->y_scale) return FQM_E_NULL;
+    if (a->y_dtype == FQM_I8 && !aligned_to(a->y_scale, 4)) return FQM_E_ALIGN;
+    if (a->cols == 0) return FQM_OK;
+    if (!a->x || !a->y) return FQM_E_NULL;
+    if (!rows_ok(a->rows, a->ld_x, a->cols) || (a->terms > 1 && !rows_ok(a->terms, a->ld_term, a->cols)) ||
+        (a->residual && !rows_ok(a->rows, a->ld_res, a->cols)) ||
+        (a->total && !rows_ok(a->rows, a->ld_total, a->cols)) || !rows_ok(a->rows, a->ld_y, a->cols))
+        return FQM_E_SHAPE;
+    const int32_t total_dtype = a->residual ? a->res_dtype : a->x_dtype;
+    if (!aligned_to(a->x, dtype_bytes(a->x_dtype)) || !aligned_to(a->y, dtype_bytes(a->y_dtype)) ||
+        (a->residual && !aligned_to(a->residual, dtype_bytes(a->res_dtype))) ||
+        (a->weight && !aligned_to(a->weight, dtype_bytes(a->weight_dtype))) ||
+        (a->total && !aligned_to(a->total, dtype_bytes(total_dtype))))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+bool norm_buffers_ok(const fqm_norm& a) {
+    const int64_t xb = dtype_bytes(a.x_dtype), rb = dtype_bytes(a.res_dtype), yb = dtype_bytes(a.y_dtype);
+    const int64_t tb = a.residual ? rb : xb;
+    const int64_t term = a.terms > 1 ? (a.terms - 1) * a.ld_term : 0;
+    return in_allocation(a.x, (span(a.rows, a.ld_x, a.cols) + term) * xb) &&
+           (!a.residual || in_allocation(a.residual, span(a.rows, a.ld_res, a.cols) * rb)) &&
+           (!a.weight || in_allocation(a.weight, a.cols * dtype_bytes(a.weight_dtype))) &&
+           (!a.total || in_allocation(a.total, span(a.rows, a.ld_total, a.cols) * tb)) &&
+           in_allocation(a.y, span(a.rows, a.ld_y, a.cols) * yb) &&
+           (a.y_dtype != FQM_I8 || in_allocation(a.y_scale, a.rows * 4));
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 24;  // rows of one lora or grouped call
+
+fqm_status check_adapters(const fqm_adapters* a) {
+    if (!a) return FQM_E_NULL;
+    if (a->count < 1 || a->count > 65536 || a->rank < 1 || a->rank > 256) return FQM_E_FORMAT;
+    if (a->rows < 0 || a->rows > kMaxRows || a->cols < 0 || a->cols > kMaxRows || a->cols % 8) return FQM_E_SHAPE;
+    if (a->rows == 0) return FQM_OK;
+    if ((a->cols > 0 && !a->A) || !a->B) return FQM_E_NULL;
+    if (!rows_ok((int64_t)a->count * a->rank, a->ld_A, a->cols) ||
+        !rows_ok((int64_t)a->count * a->rows, a->ld_B, a->rank))
+        return FQM_E_SHAPE;
+    if (!aligned16(a->A) || !aligned16(a->B) || (a->ld_A & 7) || (a->ld_B & 7) || !aligned_to(a->scale, 4) ||
+        !aligned_to(a->ranks, 4))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+fqm_status check_groups(const fqm_weights* w, const fqm_groups* g) {
+    const fqm_status st = check_weights(w);
+    if (st != FQM_OK) return st;
+    if (!lut_format(*w)) return FQM_E_UNSUPPORTED;
+    if (!g) return FQM_E_NULL;
+    if (g->count < 1 || g->count > 4096) return FQM_E_FORMAT;
+    if (!(g->x_dtype == FQM_BF16 || g->x_dtype == FQM_I8) || !value_dtype(g->y_dtype)) return FQM_E_FORMAT;
+    if (g->M < 0 || g->M > kMaxRows || g->x_rows < 0 || g->x_rows > 0x7fffffff || g->y_rows < 0 ||
+        g->y_rows > 0x7fffffff || w->rows % g->count || w->rows / g->count > kMaxRows || w->cols > kMaxRows)
+        return FQM_E_SHAPE;
+    if (g->M == 0 || w->rows == 0) return FQM_OK;
+    if ((!g->src && g->x_rows < g->M) || (!g->dst && g->y_rows < g->M)) return FQM_E_SHAPE;
+    if (g->src && g->x_rows * w->cols * 2 > INT32_MAX) return FQM_E_SHAPE;
+    const bool has_x = g->x_rows > 0 && w->cols > 0;
+    if (!g->offsets || (g->y_rows > 0 && !g->Y) || (has_x && !g->X) ||
+        (g->x_dtype == FQM_I8 && has_x && !g->x_scale))
+        return FQM_E_NULL;
+    if (!aligned16(g->X) || !aligned16(g->Y) || !aligned_to(g->offsets, 4) || !aligned_to(g->src, 4) ||
+        !aligned_to(g->dst, 4) || !aligned_to(g->x_scale, 4) || !aligned_to(g->row_scale, 4))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+bool groups_buffers_ok(const fqm_weights& w, const fqm_groups& g) {
+    return check_weight_buffers(w) == FQM_OK && in_allocation(g.offsets, ((int64_t)g.count + 1) * 4) &&
+           in_allocation(g.X, g.x_rows * w.cols * dtype_bytes(g.x_dtype)) &&
+           (g.x_dtype != FQM_I8 || in_allocation(g.x_scale, g.x_rows * 4)) && (!g.src || in_allocation(g.src, g.M * 4)) &&
+           in_allocation(g.Y, g.y_rows * (w.rows / g.count) * dtype_bytes(g.y_dtype)) &&
+           (!g.dst || in_allocation(g.dst, g.M * 4)) && (!g.row_scale || in_allocation(g.row_scale, g.M * 4));
+}
+
+}  // namespace
+
+extern "C" {
+
+fqm_status fqm_add_rms_norm(const fqm_norm* a, void* stream) {
+    const fqm_status st = check_norm(a);
+    if (st != FQM_OK || a->rows == 0) return st;
+    hipStream_t s = as_stream(stream);
+    if (a->cols == 0) {
+        if (a->y_dtype != FQM_I8) return FQM_OK;
+        if (debug_on() && !in_allocation(a->y_scale, a->rows * 4)) return FQM_E_BOUNDS;
+        return debug_finish(hip_status(launch_zero_fill(a->y_scale, a->rows, 4, s)), s);
+    }
+    if (debug_on() && !norm_buffers_ok(*a)) return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_add_rms_norm(*a, s)), s);
+}
+
+size_t fqm_lora_workspace_size(const fqm_adapters* a, int64_t M) {
+    if (check_adapters(a) != FQM_OK || M <= 0 || M > kMaxRows || a->rows == 0) return 0;
+    return fqm::lora_workspace(*a, M);
+}
+
+fqm_status fqm_lora(const fqm_adapters* a, const uint16_t* x, const int32_t* index, const void* base,
+                    int32_t base_dtype, void* y, int32_t y_dtype, int64_t M, void* workspace, size_t ws_bytes,
+                    void* stream) {
+    const fqm_status st = check_adapters(a);
+    if (st != FQM_OK) return st;
+    if (M < 0 || M > kMaxRows) return FQM_E_SHAPE;
+    if (!value_dtype(y_dtype) || (base && !value_dtype(base_dtype))) return FQM_E_FORMAT;
+    if (M == 0 || a->rows == 0) return FQM_OK;
+    if ((a->cols > 0 && !x) || !index || !y) return FQM_E_NULL;
+    if (base == y && base_dtype != y_dtype) return FQM_E_FORMAT;
+    if (!aligned16(x) || !aligned_to(index, 4) || !aligned_to(y, dtype_bytes(y_dtype)) ||
+        (base && !aligned_to(base, dtype_bytes(base_dtype))))
+        return FQM_E_ALIGN;
+    const size_t need = fqm_lora_workspace_size(a, M);
+    if (need && (!workspace || ws_bytes < need)) return FQM_E_WORKSPACE;
+    if (need && !aligned16(workspace)) return FQM_E_ALIGN;
+    hipStream_t s = as_stream(stream);
+    if (debug_on() &&
+        !(in_allocation(a->A, span((int64_t)a->count * a->rank, a->ld_A, a->cols) * 2) &&
+          in_allocation(a->B, span((int64_t)a->count * a->rows, a->ld_B, a->rank) * 2) &&
+          (!a->scale || in_allocation(a->scale, a->count * 4ll)) &&
+          (!a->ranks || in_allocation(a->ranks, a->count * 4ll)) && in_allocation(x, M * a->cols * 2) &&
+          in_allocation(index, M * 4) && (!base || in_allocation(base, M * a->rows * dtype_bytes(base_dtype))) &&
+          in_allocation(y, M * a->rows * dtype_bytes(y_dtype)) && in_allocation(workspace, (int64_t)need)))
+        return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_lora(*a, x, index, base, base_dtype == FQM_F32, y, y_dtype == FQM_F32, M,
+                                               static_cast<float*>(workspace), s)),
+                        s);
+}
+
+size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g) {
+    if (check_groups(w, g) != FQM_OK || g->M == 0 || w->rows == 0) return 0;
+    return fqm::grouped_workspace(*w, *g);
+}
+
+fqm_status fqm_gemm_grouped(const fqm_weights* w, const fqm_groups* g, void* workspace, size_t ws_bytes,
+                            void* stream) {
+    const fqm_status st = check_groups(w, g);
+    if (st != FQM_OK || g->M == 0 || w->rows == 0) return st;
+    const size_t need = fqm::grouped_workspace(*w, *g);
+    if (need && (!workspace || ws_bytes < need)) return FQM_E_WORKSPACE;
+    if (need && !aligned16(workspace)) return FQM_E_ALIGN;
+    hipStream_t s = as_stream(stream);
+    if (debug_on() && (!groups_buffers_ok(*w, *g) || (need && !in_allocation(workspace, (int64_t)need))))
+        return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_grouped(*w, *g, workspace, s)), s);
 }
 
 }  // extern "C"

@@ -1,0 +1,18 @@
+// Internal declarations of the operators around the products: the residual
+// norm, the low-rank adapters and the products grouped by expert.
+#pragma once
+
+#include "fqm_internal.h"
+
+namespace fqm {
+
+hipError_t launch_add_rms_norm(const fqm_norm& a, hipStream_t s);
+
+size_t lora_workspace(const fqm_adapters& a, int64_t M);
+hipError_t launch_lora(const fqm_adapters& a, const uint16_t* x, const int32_t* index, const void* base,
+                       int base_f32, void* y, int y_f32, int64_t M, float* ws, hipStream_t s);
+
+size_t grouped_workspace(const fqm_weights& w, const fqm_groups& g);
+hipError_t launch_grouped(const fqm_weights& w, const fqm_groups& g, void* ws, hipStream_t s);
+
+}  // namespace fqm

@@ -102,7 +102,9 @@ typedef enum fqm_status {
 } fqm_status;
 
 enum fqm_format { FQM_LUT6 = 1, FQM_FABQ = 2, FQM_MDBF = 3, FQM_LUT4 = 4 };
-enum fqm_dtype { FQM_BF16 = 0, FQM_F32 = 1 };
+/* FQM_I8 (two's complement, one fp32 scale per row) is an output of
+ * fqm_add_rms_norm and an input of fqm_gemm_grouped only. */
+enum fqm_dtype { FQM_BF16 = 0, FQM_F32 = 1, FQM_I8 = 2 };
 
 /* Per-row LUT, 6-bit codes (rows = N outputs, cols = K inputs).
  * cols must be a multiple of 64 (one 48-byte group holds 64 codes). */
@@ -315,6 +317,124 @@ size_t fqm_gemm_workspace_size(const fqm_weights* w, int64_t M);
  * FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
 fqm_status fqm_gemm(const fqm_weights* w, const uint16_t* X, uint16_t* Y, int64_t M,
                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands around the products in a decoder layer: the residual norm in
+ * front of them, the adapters beside them, and the products of many experts.
+ * Descriptors are HOST memory, read during the call only.  These three calls
+ * handle NaN and infinities as the arithmetic below gives them; bf16 outputs
+ * are rounded to nearest even.
+ * ------------------------------------------------------------------------- */
+
+/* Rows of fqm_add_rms_norm.  Strides are in elements; unlike the products,
+ * the rows here need only their element's alignment and any stride that holds
+ * a row. */
+typedef struct fqm_norm {
+    int64_t rows, cols;         /* cols 0..32768 */
+    int32_t terms;              /* 1..64 vectors of x added per row */
+    int32_t x_dtype;            /* FQM_BF16 or FQM_F32 */
+    int32_t res_dtype;          /* of residual: FQM_BF16 or FQM_F32 */
+    int32_t weight_dtype;       /* FQM_BF16 or FQM_F32 */
+    int32_t y_dtype;            /* FQM_BF16, FQM_F32 or FQM_I8 */
+    float eps;                  /* >= 0 */
+    const void* x;              /* element (row, term, col) at row*ld_x + term*ld_term + col */
+    int64_t ld_x, ld_term;      /* ld_term is not read with one term */
+    const void* residual;       /* [rows][ld_res], or NULL: none */
+    int64_t ld_res;
+    const void* weight;         /* [cols], or NULL: ones */
+    void* total;                /* [rows][ld_total], the sum, or NULL: not stored; its dtype is the
+                                   residual's, or x's without one.  May be the residual itself. */
+    int64_t ld_total;
+    void* y;                    /* [rows][ld_y] */
+    int64_t ld_y;
+    float* y_scale;             /* [rows], required for FQM_I8, not used otherwise */
+} fqm_norm;
+
+/* The residual's addition and the root-mean-square norm in one pass:
+ *     h = sum over terms of x + residual                       (fp32)
+ *     y = h * weight / sqrt(mean(h^2) + eps)
+ * total receives h rounded to its dtype (y is formed from the unrounded h).
+ * With y_dtype FQM_I8, y_scale[row] = max|y| / 127 and y holds
+ * round(y / y_scale) (nearest even, within [-127, 127]); a row of zeros has
+ * scale 0 and codes 0; a row whose scale is not finite has codes 0.
+ * rows == 0 enqueues nothing; cols == 0 writes zeros to y_scale. */
+fqm_status fqm_add_rms_norm(const fqm_norm* a, void* stream);
+
+/* `count` low-rank adapters of one projection of `cols` inputs and `rows`
+ * outputs: adapter a adds scale[a] * B_a (A_a x).  ld_A and ld_B are in
+ * elements, multiples of 8 (16 bytes). */
+typedef struct fqm_adapters {
+    int32_t count;              /* 1..65536 */
+    int32_t rank;               /* the largest rank, 1..256 */
+    int64_t rows, cols;         /* rows >= 0; cols a multiple of 8 */
+    const uint16_t* A;          /* [count][rank][ld_A] bf16, ld_A >= cols */
+    int64_t ld_A;
+    const uint16_t* B;          /* [count][rows][ld_B] bf16, ld_B >= rank */
+    int64_t ld_B;
+    const float* scale;         /* [count], or NULL: ones */
+    const int32_t* ranks;       /* [count], adapter a's own rank (values outside 0..rank are
+                                   taken as the nearest of them), or NULL: rank.  Rows of A
+                                   and columns of B from it on are not used, whatever they hold. */
+} fqm_adapters;
+
+/* Bytes of device workspace fqm_lora needs for M rows: the products A x in
+ * fp32, in parts where the columns are split over workgroups.  0 for an
+ * invalid descriptor. */
+size_t fqm_lora_workspace_size(const fqm_adapters* a, int64_t M);
+
+/* y[m] = base[m] + scale[i] * B_i (A_i x[m]) with i = index[m], each row with an
+ * adapter of its own; rows in any order.  A row whose index is outside
+ * 0..count-1 has no adapter: y[m] = base[m].
+ * x [M][cols] bf16, index [M], base [M][rows] (base_dtype FQM_BF16 or FQM_F32;
+ * NULL: zeros), y [M][rows] (y_dtype FQM_BF16 or FQM_F32), all dense.  base
+ * and y need only their element's alignment and may be the same buffer
+ * (then of the same dtype); no other buffers may overlap.
+ * A x is kept in fp32; B_i (A_i x) is formed on the matrix cores from the two
+ * leading bf16 parts of scale * A x (2^-17 relative).  workspace as for
+ * fqm_gemv.  Results do not depend on timing, nor on the other rows. */
+fqm_status fqm_lora(const fqm_adapters* a, const uint16_t* x, const int32_t* index, const void* base,
+                    int32_t base_dtype, void* y, int32_t y_dtype, int64_t M, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* Rows of fqm_gemm_grouped.  offsets, src and dst are DEVICE memory and only
+ * the kernels read them.  offsets must not decrease; none leads outside the
+ * buffers whatever it holds (each is clamped to 0..M, and a group that ends
+ * before it starts is empty). */
+typedef struct fqm_groups {
+    int32_t count;              /* groups (experts), 1..4096 */
+    const int32_t* offsets;     /* [count + 1]: group g owns the grouped rows offsets[g] .. offsets[g+1]-1 */
+    int64_t M;                  /* grouped rows (at most), 0..2^24 */
+    const void* X;              /* [x_rows][cols], dense */
+    int32_t x_dtype;            /* FQM_BF16, or FQM_I8 with x_scale */
+    int64_t x_rows;
+    const float* x_scale;       /* [x_rows] (FQM_I8) */
+    const int32_t* src;         /* [M]: grouped row i is row src[i] of X (outside 0..x_rows-1: a row of
+                                   zeros); NULL: row i (x_rows >= M) */
+    void* Y;                    /* [y_rows][rows / count], dense */
+    int32_t y_dtype;            /* FQM_BF16 or FQM_F32 */
+    int64_t y_rows;
+    const int32_t* dst;         /* [M]: grouped row i is stored to row dst[i] of Y (outside 0..y_rows-1:
+                                   not stored; no two rows may share one); NULL: row i (y_rows >= M) */
+    const float* row_scale;     /* [M]: a factor of grouped row i's output, or NULL: 1 */
+} fqm_groups;
+
+/* Bytes of device workspace fqm_gemm_grouped needs on the current device (a
+ * function of the sizes and types only, not of the offsets); 0 for invalid
+ * arguments. */
+size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g);
+
+/* Products grouped by expert: for each group e and grouped row i of it
+ *     Y[dst[i]] = row_scale[i] * (W_e X[src[i]])
+ * with `count` matrices of equal size stacked in one LUT6 or LUT4 descriptor
+ * (w->rows = count * rows of one; group e's are rows e * rows/count on) and
+ * decoded inside the kernels as in fqm_gemv and fqm_gemm.  int8 rows enter the
+ * bf16 matrix cores exactly; their scale multiplies the fp32 sum.  Rows of Y
+ * that no grouped row is stored to keep what they hold.  cols must be a
+ * multiple of 64 and, with src, x_rows * cols * 2 < 2^31; rows and cols of one
+ * matrix at most 2^24.  cols == 0 counts as sums of nothing: zeros are stored.
+ * FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
+fqm_status fqm_gemm_grouped(const fqm_weights* w, const fqm_groups* g, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 #ifdef __cplusplus
 }

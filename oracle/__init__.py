@@ -21,9 +21,11 @@ library matrix product:
           "How It Works" / "Quantization Details").
   mdbf  - multi-envelope double binary factorisation (OneCompression "MDBF",
           "Algorithm" and "Bit-width and rank").
+  layer - the operators around the products (residual norm, low-rank
+          adapters, products grouped by expert) with bounds on fp32's error.
 
 Pins that tie each part to something other than itself live in
 ``tests/test_oracle_*.py``.  Parity status per function is stated in each
 module header.
 """
-from . import numerics, bits, lut6, lut4, fabq, mdbf, compare  # noqa: F401
+from . import numerics, bits, lut6, lut4, fabq, mdbf, compare, layer  # noqa: F401
