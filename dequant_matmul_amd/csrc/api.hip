@@ -523,7 +523,7 @@ fqm_status check_groups(const fqm_weights* w, const fqm_groups* g) {
     if (g->count < 1 || g->count > 4096) return FQM_E_FORMAT;
     if (!(g->x_dtype == FQM_BF16 || g->x_dtype == FQM_I8) || !value_dtype(g->y_dtype)) return FQM_E_FORMAT;
     if (g->M < 0 || g->M > kMaxRows || g->x_rows < 0 || g->x_rows > 0x7fffffff || g->y_rows < 0 ||
-        g->y_rows > 0x7fffffff || w->rows % g->count || w->rows / g->count > kMaxRows || w->cols > kMaxRows)
+        g->y_rows > 0x7fffffff || w->rows % g->count || w->rows / g->count > kMaxRows || w->cols > (1 << 21))
         return FQM_E_SHAPE;
     if (g->M == 0 || w->rows == 0) return FQM_OK;
     if ((!g->src && g->x_rows < g->M) || (!g->dst && g->y_rows < g->M)) return FQM_E_SHAPE;

@@ -430,8 +430,8 @@ size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g
  * decoded inside the kernels as in fqm_gemv and fqm_gemm.  int8 rows enter the
  * bf16 matrix cores exactly; their scale multiplies the fp32 sum.  Rows of Y
  * that no grouped row is stored to keep what they hold.  cols must be a
- * multiple of 64 and, with src, x_rows * cols * 2 < 2^31; rows and cols of one
- * matrix at most 2^24.  cols == 0 counts as sums of nothing: zeros are stored.
+ * multiple of 64, at most 2^21, and, with src, x_rows * cols * 2 < 2^31; rows
+ * of one matrix at most 2^24.  cols == 0 counts as sums of nothing: zeros are stored.
  * FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
 fqm_status fqm_gemm_grouped(const fqm_weights* w, const fqm_groups* g, void* workspace, size_t ws_bytes,
                             void* stream);
