@@ -16,6 +16,9 @@ import torch
 from . import (FQM_BF16, FQM_F32, FQM_I8, FQM_LUT4, FQM_LUT6, _Adapters, _check, _check_workspace, _Groups, _Norm,
                _stream, _WeightsBase, load)
 
+# The current stream's handle without a Stream object around it (2.9 us a call on the host, as much as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 _CODE = {torch.bfloat16: FQM_BF16, torch.float32: FQM_F32, torch.int8: FQM_I8}
 _VALUE = (torch.bfloat16, torch.float32)
 
@@ -31,6 +34,12 @@ def _need(t, name: str, dtypes, device=None, dim: int | None = None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {dim} dimensions")
+
+
+def _handle(stream, device):
+    if stream is None and _raw_stream is not None and device.index == torch.cuda.current_device():
+        return _raw_stream(device.index)
+    return _stream(stream)
 
 
 def _vector(t, name: str, n: int, dtypes, device):
@@ -109,24 +118,26 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float
         keep_total = residual is not None or terms > 1
     if total is not None:
         _need(total, "total", (total_dtype,), dev)
+        a.ld_total, a.total = _row_stride(total, "total", (rows, cols)), total.data_ptr()
     elif keep_total:
         total = torch.empty((rows, cols), dtype=total_dtype, device=dev)
-    if total is not None:
-        a.ld_total, a.total = _row_stride(total, "total", (rows, cols)), total.data_ptr()
+        a.ld_total, a.total = cols, total.data_ptr()
     if y is None:
         if out_dtype not in _CODE:
             raise ValueError(f"out_dtype must be bfloat16, float32 or int8, not {out_dtype}")
         y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        a.ld_y = cols
     else:
         _need(y, "y", tuple(_CODE), dev)
-    a.ld_y, a.y, a.y_dtype = _row_stride(y, "y", (rows, cols)), y.data_ptr(), _CODE[y.dtype]
-    if y.dtype == torch.int8:
+        a.ld_y, out_dtype = _row_stride(y, "y", (rows, cols)), y.dtype
+    a.y, a.y_dtype = y.data_ptr(), _CODE[out_dtype]
+    if out_dtype == torch.int8:
         if scale is None:
             scale = torch.empty(rows, dtype=torch.float32, device=dev)
         a.y_scale = _vector(scale, "scale", rows, (torch.float32,), dev)
     else:
         scale = None
-    _check(load().fqm_add_rms_norm(ctypes.byref(a), _stream(stream)), "fqm_add_rms_norm")
+    _check(load().fqm_add_rms_norm(ctypes.byref(a), _handle(stream, dev)), "fqm_add_rms_norm")
     return NormOut(y, scale, total)
 
 
@@ -235,7 +246,7 @@ def lora(adapters: Adapters, x: torch.Tensor, index: torch.Tensor, base: torch.T
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.fqm_lora(adapters.ref, x.data_ptr(), ip, bp, bdt, y.data_ptr(), _CODE[y.dtype], M,
-                        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream)),
+                        workspace.data_ptr() if workspace is not None else None, ws_bytes, _handle(stream, dev)),
            "fqm_lora")
     return y
 
@@ -319,5 +330,5 @@ def gemm_grouped(w: _WeightsBase, X: torch.Tensor, offsets: torch.Tensor, src: t
         workspace = torch.empty(need, dtype=torch.uint8, device=Y.device) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.fqm_gemm_grouped(w.ref, ctypes.byref(g), workspace.data_ptr() if workspace is not None else None,
-                                ws_bytes, _stream(stream)), "fqm_gemm_grouped")
+                                ws_bytes, _handle(stream, Y.device)), "fqm_gemm_grouped")
     return Y

@@ -503,10 +503,10 @@ constexpr int64_t kMaxRows = (int64_t)1 << 24;  // rows of one lora or grouped c
 fqm_status check_adapters(const fqm_adapters* a) {
     if (!a) return FQM_E_NULL;
     if (a->count < 1 || a->count > 65536 || a->rank < 1 || a->rank > 256) return FQM_E_FORMAT;
-    if (a->rows < 0 || a->rows > kMaxRows || a->cols < 0 || a->cols > kMaxRows || a->cols % 8) return FQM_E_SHAPE;
+    if (a->rows < 0 || a->rows > (1 << 22) || a->cols < 0 || a->cols > (1 << 21) || a->cols % 8) return FQM_E_SHAPE;
     if (a->rows == 0) return FQM_OK;
     if ((a->cols > 0 && !a->A) || !a->B) return FQM_E_NULL;
-    if (!rows_ok((int64_t)a->count * a->rank, a->ld_A, a->cols) ||
+    if (!rows_ok((int64_t)a->count * a->rank, a->ld_A, a->cols) || a->ld_A > (1 << 22) ||
         !rows_ok((int64_t)a->count * a->rows, a->ld_B, a->rank))
         return FQM_E_SHAPE;
     if (!aligned16(a->A) || !aligned16(a->B) || (a->ld_A & 7) || (a->ld_B & 7) || !aligned_to(a->scale, 4) ||

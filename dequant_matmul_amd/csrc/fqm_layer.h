@@ -6,6 +6,15 @@
 
 namespace fqm {
 
+// Workgroup barrier for LDS alone: LDS operations are complete, global loads
+// and stores of the wave stay in flight (__syncthreads waits for them too).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 hipError_t launch_add_rms_norm(const fqm_norm& a, hipStream_t s);
 
 size_t lora_workspace(const fqm_adapters& a, int64_t M);

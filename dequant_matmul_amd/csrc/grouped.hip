@@ -271,11 +271,6 @@ __global__ __launch_bounds__(64 * kRowWaves) void grouped_rows_kernel(const Grou
     const uint32_t tab = (uint32_t)(uintptr_t)(lds8*)s_tab + 128u * kMaxR * wave;
     for (int i0 = lo; i0 < hi; i0 += bmax) {
         const int nrows = min(bmax, hi - i0);
-        uint32_t cr[kAhead][BITS / 2];
-        if (pieces > 0) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) load_piece<BITS>(W.row(min(u / chunks, R - 1)), u % chunks, pieces, cr[u]);
-        }
         int xr[kMaxB];
 #pragma unroll
         for (int b = 0; b < kMaxB; ++b) xr[b] = b < nrows ? x_row(g, i0 + b) : -1;
@@ -283,21 +278,28 @@ __global__ __launch_bounds__(64 * kRowWaves) void grouped_rows_kernel(const Grou
             for (int r = 0; r < R; ++r)
                 s_tab[wave][r][lane] = a.lut[((int64_t)e * a.N + min(W.number(r), a.N - 1)) * ENTRIES + lane];
         }
-        __syncthreads();  // the last pass is done with s_x
-        // 16-byte unit u = 128 c + 2 l + h of a row goes to slot 128 c + 64 h + l: a wave's reads are dense
-        for (int u = tid; u < a.K / 8; u += NT) {
+        lds_barrier();  // the last pass is done with s_x
+        // 16-byte unit u = 128 c + 2 l + h of a row goes to slot 128 c + 64 h + l: a wave's reads are dense.  The
+        // first codes are requested behind the last of X's loads, and only the latter are waited for.
+        uint32_t cr[kAhead][BITS / 2];
+        for (int u0 = 0; u0 < a.K / 8; u0 += NT) {
+            const int u = u0 + tid, units = a.K / 8;
             u32x4_t v[kMaxB];
 #pragma unroll
             for (int b = 0; b < kMaxB; ++b) {
                 v[b] = u32x4_t{0u, 0u, 0u, 0u};
-                if (b < nrows && xr[b] >= 0) v[b] = load_x8(g, (int64_t)xr[b] * a.K + 8 * u);
+                if (u < units && xr[b] >= 0) v[b] = load_x8(g, (int64_t)xr[b] * a.K + 8 * u);
+            }
+            if (u0 + NT >= units) {
+#pragma unroll
+                for (int s = 0; s < kAhead; ++s) load_piece<BITS>(W.row(min(s / chunks, R - 1)), s % chunks, pieces, cr[s]);
             }
             const int slot16 = (u & ~127) | (u & 1) << 6 | ((u >> 1) & 63);
 #pragma unroll
             for (int b = 0; b < kMaxB; ++b)
-                if (b < nrows) *(lds_u4*)(uintptr_t)(xs + stride * b + 16u * slot16) = v[b];
+                if (u < units && b < nrows) *(lds_u4*)(uintptr_t)(xs + stride * b + 16u * slot16) = v[b];
         }
-        __syncthreads();
+        lds_barrier();
         if (pieces == 0) {  // sums of nothing
             if (lane < kMaxR * kMaxB) s_sum[wave][lane / kMaxB][lane % kMaxB] = 0.f;
         } else if (nrows == 1) dot_rows<BITS, 1>(W, R, tab, xs, stride, pieces, cr, s_sum[wave]);

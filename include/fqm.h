@@ -366,8 +366,8 @@ fqm_status fqm_add_rms_norm(const fqm_norm* a, void* stream);
 typedef struct fqm_adapters {
     int32_t count;              /* 1..65536 */
     int32_t rank;               /* the largest rank, 1..256 */
-    int64_t rows, cols;         /* rows >= 0; cols a multiple of 8 */
-    const uint16_t* A;          /* [count][rank][ld_A] bf16, ld_A >= cols */
+    int64_t rows, cols;         /* rows 0..2^22; cols a multiple of 8, at most 2^21 */
+    const uint16_t* A;          /* [count][rank][ld_A] bf16, cols <= ld_A <= 2^22 */
     int64_t ld_A;
     const uint16_t* B;          /* [count][rows][ld_B] bf16, ld_B >= rank */
     int64_t ld_B;
@@ -389,9 +389,10 @@ size_t fqm_lora_workspace_size(const fqm_adapters* a, int64_t M);
  * NULL: zeros), y [M][rows] (y_dtype FQM_BF16 or FQM_F32), all dense.  base
  * and y need only their element's alignment and may be the same buffer
  * (then of the same dtype); no other buffers may overlap.
- * A x is kept in fp32; B_i (A_i x) is formed on the matrix cores from the two
- * leading bf16 parts of scale * A x (2^-17 relative).  workspace as for
- * fqm_gemv.  Results do not depend on timing, nor on the other rows. */
+ * A x is kept in fp32; B_i (A_i x) is formed on the matrix cores from scale * A x
+ * as a sum of bf16 terms, exact to 2^-17 of it for a bf16 y and to 2^-25 for an
+ * fp32 y.  workspace as for fqm_gemv.  Results do not depend on timing, nor on
+ * the other rows' values. */
 fqm_status fqm_lora(const fqm_adapters* a, const uint16_t* x, const int32_t* index, const void* base,
                     int32_t base_dtype, void* y, int32_t y_dtype, int64_t M, void* workspace,
                     size_t ws_bytes, void* stream);

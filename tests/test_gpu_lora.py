@@ -177,3 +177,24 @@ def test_another_stream_and_graph_replays():
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("M,count,rank,K,N,kind,base,out", [
+    (100, 3, 256, 264, 300, "runs", "bf16", "bf16"),
+    (65, 64, 256, 72, 1030, "any", "f32", "f32"),
+    (130, 2, 17, 5128, 64, "runs", None, "bf16"),
+    (1000, 3, 16, 40, 63, "any", "bf16", "f32"),
+])
+def test_wide_ranks_and_narrow_layers_in_blocks_of_rows(M, count, rank, K, N, kind, base, out):
+    print(f"lora blocks M {M} count {count} rank {rank} {K}->{N}", flush=True)
+    rng = np.random.default_rng([M, rank, K])
+    ad, parts = pool(count, rank, K, N, seed=M)
+    x = bf16_dev(synth.activations(M, K, 5))
+    index = order(kind, M, count, rng)
+    b = torch.from_numpy(rng.standard_normal((M, N))).to(DEV).to(T[base]) if base else None
+    buf, y = guarded((M, N), T[out])
+    fqm.lora(ad, x, torch.from_numpy(index.astype(np.int32)).to(DEV), base=b, y=y)
+    torch.cuda.synchronize()
+    assert canaries_intact(buf)
+    yo, lim = want(parts, x, index, b)
+    assert (np.abs(to_f64(y) - yo) <= oracle.layer.rounded(lim, yo, out)).all()
