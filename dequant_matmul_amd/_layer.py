@@ -4,7 +4,8 @@ low-rank adapters and the products grouped by expert.
 Argument marshalling only, as in the package's other calls: shapes, types,
 layouts and devices are checked here (the C ABI sees only pointers), the
 computation runs in the HIP kernels behind ``fqm_add_rms_norm``, ``fqm_lora``
-and ``fqm_gemm_grouped`` (include/fqm.h has their definitions).
+and ``fqm_gemm_grouped`` (include/fqm.h has their definitions).  With ``stream``
+given, what a call allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -36,10 +37,31 @@ def _need(t, name: str, dtypes, device=None, dim: int | None = None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {dim} dimensions")
 
 
-def _handle(stream, device):
-    if stream is None and _raw_stream is not None and device.index == torch.cuda.current_device():
-        return _raw_stream(device.index)
-    return _stream(stream)
+def _elsewhere(stream, device):
+    """Whether the call is for another stream or device than the current ones.  It is then
+    made again inside them: what it allocates (outputs, workspace) belongs to that stream,
+    so that its memory is not handed out again under the running kernels."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+class _inside:
+    """The device and stream of a call as the current ones."""
+
+    def __init__(self, stream, device):
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _handle(device):
+    return _raw_stream(device.index) if _raw_stream is not None else _stream()
 
 
 def _vector(t, name: str, n: int, dtypes, device):
@@ -92,6 +114,9 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float
     out_dtype: bfloat16, float32, or int8 with one scale a row:
     ``scale = max|y| / 127``, ``y`` the nearest codes."""
     _need(x, "x", _VALUE)
+    if _elsewhere(stream, x.device):
+        with _inside(stream, x.device):
+            return add_rms_norm(x, weight, eps, residual, out_dtype, y, scale, total, keep_total)
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be [rows][cols] or [rows][terms][cols]; got shape {tuple(x.shape)}")
     dev, rows, cols = x.device, x.shape[0], x.shape[-1]
@@ -137,7 +162,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float
         a.y_scale = _vector(scale, "scale", rows, (torch.float32,), dev)
     else:
         scale = None
-    _check(load().fqm_add_rms_norm(ctypes.byref(a), _handle(stream, dev)), "fqm_add_rms_norm")
+    _check(load().fqm_add_rms_norm(ctypes.byref(a), _handle(dev)), "fqm_add_rms_norm")
     return NormOut(y, scale, total)
 
 
@@ -217,6 +242,9 @@ def lora(adapters: Adapters, x: torch.Tensor, index: torch.Tensor, base: torch.T
     ``y`` may be ``base`` (the addition in place).  Any M: single tokens and
     prompts, mixed."""
     _need(x, "x", (torch.bfloat16,), adapters.device, dim=2)
+    if _elsewhere(stream, x.device):
+        with _inside(stream, x.device):
+            return lora(adapters, x, index, base, y, out_dtype, workspace)
     M = x.shape[0]
     dev = x.device
     if x.shape[1] != adapters.cols or not x.is_contiguous():
@@ -246,7 +274,7 @@ def lora(adapters: Adapters, x: torch.Tensor, index: torch.Tensor, base: torch.T
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.fqm_lora(adapters.ref, x.data_ptr(), ip, bp, bdt, y.data_ptr(), _CODE[y.dtype], M,
-                        workspace.data_ptr() if workspace is not None else None, ws_bytes, _handle(stream, dev)),
+                        workspace.data_ptr() if workspace is not None else None, ws_bytes, _handle(dev)),
            "fqm_lora")
     return y
 
@@ -322,6 +350,9 @@ def gemm_grouped(w: _WeightsBase, X: torch.Tensor, offsets: torch.Tensor, src: t
     Y: [y_rows][rows of one matrix] bf16 or fp32; rows that nothing is stored
     to keep what they hold (a Y made here: undefined).  All index tensors stay on
     the GPU; nothing waits for them."""
+    if isinstance(X, torch.Tensor) and X.is_cuda and _elsewhere(stream, X.device):
+        with _inside(stream, X.device):
+            return gemm_grouped(w, X, offsets, src, x_scale, dst, row_scale, Y, out_dtype, y_rows, workspace)
     g, Y = _groups(w, X, offsets, src, x_scale, dst, row_scale, Y, out_dtype, y_rows)
     _check_workspace(workspace, Y.device)
     lib = load()
@@ -330,5 +361,5 @@ def gemm_grouped(w: _WeightsBase, X: torch.Tensor, offsets: torch.Tensor, src: t
         workspace = torch.empty(need, dtype=torch.uint8, device=Y.device) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.fqm_gemm_grouped(w.ref, ctypes.byref(g), workspace.data_ptr() if workspace is not None else None,
-                                ws_bytes, _handle(stream, Y.device)), "fqm_gemm_grouped")
+                                ws_bytes, _handle(Y.device)), "fqm_gemm_grouped")
     return Y

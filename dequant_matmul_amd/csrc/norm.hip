@@ -8,9 +8,10 @@
 // need no second reduction: y's row factor r = 1/sqrt(...) is common, so
 // max|y| = r * max|h w| and y / scale = h w * 127 / max|h w|.
 //
-// What binds it: memory for many rows, the launch and two dependent memory
-// round trips (loads, then stores) for few.  Sums, statistics and scales are fp32; h is
-// rounded only where total is stored.
+// What binds it, on one MI355X: memory for many rows (8192 x 5120 bf16 59.9 us, 5.6
+// TB/s; 4096 x 8 terms x 5120 to 8 bits 92 us, 4.8 TB/s), the launch and two
+// dependent memory round trips (loads, then stores) for few (1 x 5120 3.6 us).
+// Sums, statistics and scales are fp32; h is rounded only where total is stored.
 #include <algorithm>
 
 #include "fqm_layer.h"
@@ -114,8 +115,8 @@ __device__ __forceinline__ void store_i8(void* p, int64_t e, const int (&c)[kVec
     }
 }
 
-// One row per threadIdx.y; blockDim.x threads per row (a multiple of 64, so a
-// wave never spans rows), NV chunks each.  XF32, RF32: the types of x and of
+// One row per threadIdx.y; blockDim.x threads per row (16, 32, or a multiple of
+// 64: a row's lanes are a part of one wave or whole waves), NV chunks each.  XF32, RF32: the types of x and of
 // residual (total has the residual's type, or x's without one).
 template <int NV, bool XF32, bool RF32>
 __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_norm a) {
@@ -218,9 +219,12 @@ __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_nor
             // fmaxf passes a NaN over: an 8-bit row with one (or an infinity) gets a NaN for its scale here
             if (a.y_dtype == FQM_I8) sq = fmaf(w[v][i], 0.f, sq);
         }
-    sq = wave_sum(sq);
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+    for (int o = 32; o >= 1; o >>= 1)
+        if (nt > o) {  // over the row's lanes (uniform)
+            sq += __shfl_xor(sq, o, 64);
+            mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+        }
     if (nt > 64) {  // uniform over the grid: then one row per block
         const int wave = threadIdx.x >> 6, waves = nt >> 6;
         if ((threadIdx.x & 63) == 0) s_sq[wave] = sq, s_mx[wave] = mx;
@@ -290,12 +294,16 @@ hipError_t launch_nv(const fqm_norm& a, dim3 grid, dim3 block, hipStream_t s) {
 
 }  // namespace
 
-// One chunk per thread as far as 1024 threads reach (the fewest dependent
-// steps); rows of one wave share a 256-thread block.
+// Threads per row: a chunk each as far as 1024 threads reach (the fewest
+// dependent steps); three chunks each for many rows of a single term (8192 x
+// 5120 in bf16, 67.5 -> 59.9 us, 5.6 TB/s; eight terms would lose 9 %).  Rows of one
+// wave or less share a 256-thread block.
 hipError_t launch_add_rms_norm(const fqm_norm& a, hipStream_t s) {
     const int chunks = (int)((a.cols + kVec - 1) / kVec);
-    const int nt = std::min(kMaxThreads, (chunks + 63) / 64 * 64);
-    const int rpb = nt == 64 ? 4 : 1;
+    const int per = a.rows >= 2048 && a.terms == 1 ? 3 : 1;
+    const int want = (chunks + per - 1) / per;
+    const int nt = chunks <= 16 ? 16 : chunks <= 32 ? 32 : std::min(kMaxThreads, (want + 63) / 64 * 64);
+    const int rpb = nt <= 64 ? 256 / nt : 1;
     const int64_t blocks = (a.rows + rpb - 1) / rpb;
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block((unsigned)nt, (unsigned)rpb);

@@ -198,3 +198,65 @@ def test_wide_ranks_and_narrow_layers_in_blocks_of_rows(M, count, rank, K, N, ki
     assert canaries_intact(buf)
     yo, lim = want(parts, x, index, b)
     assert (np.abs(to_f64(y) - yo) <= oracle.layer.rounded(lim, yo, out)).all()
+
+
+@pytest.mark.parametrize("M,count,rank,K,N,kind,base,out,mixed", [
+    (321, 3, 256, 264, 200, "runs", "bf16", "f32", False),
+    (260, 2, 100, 1096, 131, "runs", "f32", "bf16", True),
+    (400, 5, 64, 648, 1025, "any", None, "bf16", True),
+    (290, 4, 40, 56, 130, "runs", "bf16", "bf16", False),
+    (700, 2, 33, 2056, 77, "one", "f32", "f32", False),
+    (257, 3, 16, 320, 512, "none", "bf16", "bf16", False),
+])
+def test_many_rows_of_all_ranks_and_types(M, count, rank, K, N, kind, base, out, mixed):
+    print(f"lora many rows M {M} count {count} rank {rank} {K}->{N} {kind} {base} {out}", flush=True)
+    rng = np.random.default_rng([M, rank, K])
+    ad, parts = pool(count, rank, K, N, seed=M, mixed=mixed, scale=M % 2 == 0)
+    x = bf16_dev(synth.activations(M, K, 5))
+    index = order(kind, M, count, rng)
+    b = torch.from_numpy(rng.standard_normal((M, N))).to(DEV).to(T[base]) if base else None
+    buf, y = guarded((M, N), T[out])
+    fqm.lora(ad, x, torch.from_numpy(index.astype(np.int32)).to(DEV), base=b, y=y)
+    torch.cuda.synchronize()
+    assert canaries_intact(buf)
+    yo, lim = want(parts, x, index, b)
+    assert (np.abs(to_f64(y) - yo) <= oracle.layer.rounded(lim, yo, out)).all()
+
+
+def test_many_rows_keep_to_themselves_and_to_their_ranks():
+    """What is not finite in a row of x, past an adapter's rank, or in another adapter, touches nothing else."""
+    M, K, N = 300, 328, 140
+    A = torch.randn(4, 20, K, device=DEV).to(torch.bfloat16)
+    B = torch.randn(4, N, 20, device=DEV).to(torch.bfloat16)
+    ranks = torch.tensor([7, 0, 55, 20], dtype=torch.int32, device=DEV)
+    index = (torch.arange(M, dtype=torch.int32, device=DEV) % 5) - 1
+    x = torch.randn(M, K, device=DEV).to(torch.bfloat16)
+    base = torch.randn(M, N, device=DEV).to(torch.bfloat16)
+    clean = fqm.lora(fqm.Adapters(A, B, ranks=ranks), x, index, base=base)
+    A[0, 7:], B[0, :, 7:], A[1], B[1], A[3, 2, 5] = (float("nan"),) * 5
+    x[11, 3] = float("inf")
+    y = fqm.lora(fqm.Adapters(A, B, ranks=ranks), x, index, base=base)
+    keep = index != 3
+    keep[11] = False
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.equal(y[index == 1], base[index == 1]) and torch.equal(y[index == -1], base[index == -1])
+    assert torch.isnan(y[index == 3]).all()
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_a_stream_of_its_own_gets_its_own_memory(M):
+    """Outputs and workspace of a call on another stream are that stream's: work that the current
+    stream does meanwhile does not get their memory."""
+    ad, _ = pool(4, 16, 1024, 300)
+    x = torch.randn(M, 1024, device=DEV).to(torch.bfloat16)
+    index = torch.arange(M, dtype=torch.int32, device=DEV) % 4
+    ref = fqm.lora(ad, x, index)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ys = []
+    for _ in range(8):
+        ys.append(fqm.lora(ad, x, index, stream=side))
+        for n in (1 << 12, 1 << 16, 1 << 20):
+            torch.full((n,), float("nan"), device=DEV)
+    side.synchronize()
+    assert all(torch.equal(y, ref) for y in ys)

@@ -167,3 +167,18 @@ def test_another_stream_and_graph_replays():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want.y) and torch.equal(total, want.total)
+
+
+@pytest.mark.parametrize("rows,cols,out", [(2048, 5120, "bf16"), (2500, 1000, "i8"), (2049, 17416, "f32"), (4097, 128, "bf16"),
+                                           (3001, 100, "i8"), (70, 129, "f32"), (33, 256, "i8"), (5, 257, "bf16"), (2100, 8, "f32")])
+def test_many_rows_and_rows_of_part_of_a_wave(rows, cols, out):
+    """The forms with several chunks a thread and several rows a wave, a sample of the rows checked."""
+    print(f"add_rms_norm {rows}x{cols} {out}", flush=True)
+    xs, rs, w = case(rows, cols, 1, "bf16", "f32")
+    buf, y = guarded((rows, cols), T[out], fill=-123.0)
+    got = fqm.add_rms_norm(xs, w, eps=1e-5, residual=rs, y=y)
+    torch.cuda.synchronize()
+    assert canaries_intact(buf, fill=-123.0)
+    pick = sorted({r for r in (0, 1, 2, 3, 15, rows // 2, rows // 3, rows - 17, rows - 2, rows - 1) if 0 <= r < rows})
+    part = fqm.NormOut(got.y[pick], None if got.scale is None else got.scale[pick], got.total[pick])
+    check(xs[pick], rs[pick], w, float(np.float32(1e-5)), out, part, "f32")
