@@ -173,9 +173,10 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_few(const Lora p) {
 // ---- t = A x, many rows -------------------------------------------------------------
 // A workgroup: 64 rows of x times 16 RB rows of an adapter's A over one K part,
 // 64 columns a step.  Both tiles come by direct global -> LDS loads (1 KB: 8
-// rows of 128 bytes, 16-byte chunks XOR-swizzled by (row / 2) % 8) two steps
-// ahead in three buffers; a wave contracts its 16 rows of x.  Columns past the
+// rows of 128 bytes, 16-byte chunks XOR-swizzled by (row / 2) % 8) four steps
+// ahead in five buffers; a wave contracts its 16 rows of x.  Columns past the
 // last whole step (K is a multiple of 8) go through registers.
+constexpr int kRing = 5;
 template <int RB>
 struct ShrinkTile {
     static constexpr int X_BYTES = 64 * 128, BYTES = X_BYTES + 16 * RB * 128;
@@ -187,9 +188,8 @@ struct ShrinkTile {
 __device__ __forceinline__ int chunk_at(int row, int chunk) { return 128 * row + 16 * (chunk ^ ((row >> 1) & 7)); }
 
 template <int RB>
-__device__ __forceinline__ void shrink_block(lds8* b0, lds8* b1, lds8* b2, const Lora& p, int tiles) {
+__device__ __forceinline__ void shrink_block(lds8* const (&BUF)[kRing], const Lora& p, int tiles) {
     using S = ShrinkTile<RB>;
-    lds8* const BUF[3] = {b0, b1, b2};
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, col = lane & 15, K = (int)p.a.cols;
     int b = blockIdx.x;
@@ -252,25 +252,27 @@ __device__ __forceinline__ void shrink_block(lds8* b0, lds8* b1, lds8* b2, const
             }
         };
         if (t0 < t1) {
-            // Step t is in buffer (t - t0) % 3.  Before its barrier each wave waits for its own loads of
-            // step t (those of t + 1 may be in flight); after it every wave has used step t - 1, whose
-            // buffer takes step t + 2.  Past the end the last step is loaded again, and not used.
+            // Step t is in buffer (t - t0) % kRing.  Before its barrier each wave waits for its own loads of
+            // step t (those of the kAhead - 1 steps after it may be in flight); after it every wave has used
+            // step t - 1, whose buffer takes step t + kAhead.  Past the end the last step is loaded again, and
+            // not used.
+            constexpr int kAhead = kRing - 1;
             __syncthreads();  // the last adapter's steps are used
-            request(0, t0);
-            request(1, min(t0 + 1, t1 - 1));
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s) request(s, min(t0 + s, t1 - 1));
             auto step = [&](int buf, int t) {
-                barrier_after_loads<S::LOADS>();
-                request((buf + 2) % 3, min(t + 2, t1 - 1));
+                barrier_after_loads<(kAhead - 1) * S::LOADS>();
+                request((buf + kAhead) % kRing, min(t + kAhead, t1 - 1));
                 contract(buf);
             };
             int t = t0;
-            for (; t + 2 < t1; t += 3) {
-                step(0, t);
-                step(1, t + 1);
-                step(2, t + 2);
+            for (; t + kRing - 1 < t1; t += kRing) {
+#pragma unroll
+                for (int s = 0; s < kRing; ++s) step(s, t + s);
             }
-            if (t < t1) step(0, t);
-            if (t + 1 < t1) step(1, t + 1);
+#pragma unroll
+            for (int s = 0; s < kRing - 1; ++s)
+                if (t + s < t1) step(s, t + s);
             __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may still be writing LDS
         }
         const bool mine = rows >> (16 * wave + col) & 1;
@@ -302,7 +304,10 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_blocks(const Lora p, 
     __shared__ __attribute__((aligned(16))) uint8_t s_0[ShrinkTile<RB>::BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t s_1[ShrinkTile<RB>::BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t s_2[ShrinkTile<RB>::BYTES];
-    shrink_block<RB>((lds8*)s_0, (lds8*)s_1, (lds8*)s_2, p, tiles);
+    __shared__ __attribute__((aligned(16))) uint8_t s_3[ShrinkTile<RB>::BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t s_4[ShrinkTile<RB>::BYTES];
+    lds8* const buf[kRing] = {(lds8*)s_0, (lds8*)s_1, (lds8*)s_2, (lds8*)s_3, (lds8*)s_4};
+    shrink_block<RB>(buf, p, tiles);
 }
 
 // ---- y = base + B t ---------------------------------------------------------------
