@@ -310,7 +310,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void grouped_rows_kernel(const Grou
         const int b = lane % kMaxB, r = lane / kMaxB;
         if (r < R && b < nrows) {
             const int i = i0 + b, n = W.number(r), yr = y_row(g, i);
-            if (n < a.N && yr >= 0) store_y(g, (int64_t)yr * a.N + n, s_sum[wave][r][b] * row_factor(g, i, x_row(g, i)));
+            const int from = x_row(g, i);
+            const bool none = from < 0 || pieces == 0;  // zeros, whatever the factors and tables hold
+            if (n < a.N && yr >= 0) store_y(g, (int64_t)yr * a.N + n, none ? 0.f : s_sum[wave][r][b] * row_factor(g, i, from));
         }
     }
 }

@@ -409,8 +409,9 @@ typedef struct fqm_groups {
     int32_t x_dtype;            /* FQM_BF16, or FQM_I8 with x_scale */
     int64_t x_rows;
     const float* x_scale;       /* [x_rows] (FQM_I8) */
-    const int32_t* src;         /* [M]: grouped row i is row src[i] of X (outside 0..x_rows-1: a row of
-                                   zeros); NULL: row i (x_rows >= M) */
+    const int32_t* src;         /* [M]: grouped row i is row src[i] of X (outside 0..x_rows-1: none, its
+                                   row of Y is zeros whatever row_scale and the tables
+                                   hold); NULL: row i (x_rows >= M) */
     void* Y;                    /* [y_rows][rows / count], dense */
     int32_t y_dtype;            /* FQM_BF16 or FQM_F32 */
     int64_t y_rows;

@@ -174,6 +174,24 @@ def test_what_is_not_finite_stays_in_its_row(M):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("M", [4, 160])
+def test_a_row_without_x_is_zeros_whatever_is_not_finite(M):
+    w, _ = experts(6, 2, 80, 256)
+    w.lut[:80, 3] = 0x7F80  # infinity in the first expert's tables
+    x = bf16_dev(synth.activations(M, 256, 1))
+    src = np.arange(M)
+    src[::2] = -1
+    scale = torch.full((M,), float("nan"), device=DEV)
+    Y = torch.full((M, 80), 7.0, device=DEV)
+    fqm.gemm_grouped(w, x, i32([0, M // 2, M]), src=i32(src), row_scale=scale, Y=Y)
+    assert (Y[::2] == 0).all() and torch.isnan(Y[1::2]).all()
+    # no columns: zeros too
+    none = fqm.Lut6Weights(w.packed, w.lut, 160, 0)
+    Y.fill_(7.0)
+    fqm.gemm_grouped(none, x[:, :0].contiguous(), i32([0, M // 2, M]), row_scale=scale, Y=Y)
+    assert (Y == 0).all()
+
+
 def test_one_group_agrees_with_the_plain_product():
     w, W = experts(6, 1, 300, 512)
     x = bf16_dev(synth.activations(70, 512, 2))
