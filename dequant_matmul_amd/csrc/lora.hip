@@ -261,6 +261,7 @@ __device__ __forceinline__ void shrink_block(lds8* const (&BUF)[kRing], const Lo
 #pragma unroll
             for (int s = 0; s < kAhead; ++s) request(s, min(t0 + s, t1 - 1));
             auto step = [&](int buf, int t) {
+                __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): step t - 1 is read, not just requested
                 barrier_after_loads<(kAhead - 1) * S::LOADS>();
                 request((buf + kAhead) % kRing, min(t + kAhead, t1 - 1));
                 contract(buf);
