@@ -10,10 +10,11 @@
 // touches no other row.
 //
 // What binds it, on one MI355X: many rows - reading base and writing y (4096 rows,
-// 16 adapters of rank 64, 5120 -> 17408 in bf16: 130 us for 373 MB, 2.9 TB/s; at
-// rank 16 101 us); few rows - two launches and the latency of the loads in them
-// (1 row, rank 16, 5120 -> 17408: 4.4 + 6.8 us; 48 rows over 32 adapters,
-// 17408 -> 5120: 13 + 8 us for 29 MB).
+// 16 adapters of rank 64, 5120 -> 17408 in bf16: 30 us for the first launch, 100 us
+// for the second, 122 us among other calls, 373 MB at 3.1 TB/s; 17408 -> 5120 115
+// us); few rows - two launches and the latency of the loads in them (1 row, rank
+// 16, 5120 -> 17408: 4.2 + 7.4 us; 48 rows over 32 adapters, 17408 -> 5120: 13 + 9
+// us for 29 MB).
 #include <algorithm>
 
 #include "fqm_layer.h"
@@ -670,7 +671,8 @@ struct LoraPlan {
 
 // K parts: as many as fill the chip (512 workgroups of a job's four stretches
 // or 256 of 64-row blocks), each of at least four steps, few enough that adding
-// them up again stays small (4096 rows, rank 64, 4 / 12 / 24 parts: 163 / 200 / 220 us).
+// them up again stays small (4096 rows, rank 64, aimed at 256 / 512 / 768
+// workgroups: 129 / 137 / 143 us).
 LoraPlan lora_plan(const fqm_adapters& a, int64_t M) {
     LoraPlan p;
     p.few = M <= kFewRows;

@@ -4,7 +4,9 @@
  * The library computes the weight-only quantized products y = W x (GEMV,
  * batch 1..16) and Y = X W^T (GEMM) where W is stored in one of three packed
  * formats and is decoded inside the kernels; W is never written out in full
- * (fqm_dequant exists for testing only).
+ * (fqm_dequant exists for testing only).  Around them it has the residual norm
+ * (fqm_add_rms_norm), low-rank adapters beside a product (fqm_lora) and
+ * products grouped by expert (fqm_gemm_grouped).
  *
  * Formats (pages named by title and section):
  *   FQM_LUT6  "Qwen3.8-27B - BenQ 6-bit", "What BenQ stores": one 6-bit code
