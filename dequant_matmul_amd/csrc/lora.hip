@@ -41,7 +41,6 @@ struct Lora {
     float* part;  // [ksplit][M][ldt]
     int ldt;      // rank rounded up to 16
     int ksplit;
-    int terms;    // bf16 terms of t
 };
 
 __device__ __forceinline__ int rank_of(const fqm_adapters& a, int i) {
@@ -315,13 +314,15 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_blocks(const Lora p, 
 // ---- y = base + B t ---------------------------------------------------------------
 // The rows' t = scale * (sum of the K parts) goes to LDS as bf16 terms, t_0 =
 // bf16(t), t_1 = bf16(t - t_0), t_2 = bf16(t - t_0 - t_1), each against the same
-// B, smallest first.  The products are exact in fp32.  A bf16 y takes two terms
-// (what is left out is at most 2^-17 of t), an fp32 y all three (2^-25).  In a
-// pass of 128 outputs every distinct adapter's B meets the block's rows and
-// its own rows' sums go to a tile in LDS; then base streams through it to y in
-// whole lines, the next pass's base already requested.  (Straight from the
-// matrix layout, 16 rows a load, the same took 1.5 to 2 times as long with
-// many rows.)
+// B, smallest first.  The products are exact in fp32, and the three terms are t
+// to 2^-25 of it, whatever y's type (two terms would leave 2^-17, enough to turn
+// the rounding of some bf16 outputs).  In a pass of 128 outputs every distinct
+// adapter's B meets the block's rows and its own rows' sums go to a tile in LDS;
+// then base streams through it to y in whole lines, the next pass's base already
+// requested.  (Straight from the matrix layout, 16 rows a load, the same took 1.5
+// to 2 times as long with many rows.)
+constexpr int kTerms = 3;
+
 enum BaseKind { kNoBase = 0, kBaseBf16 = 1, kBaseF32 = 2 };
 
 // 8 consecutive values of base as loaded, from value `at` on (a pointer that is
@@ -393,11 +394,10 @@ __device__ __forceinline__ void store8(void* y, int f32, uint32_t at, const floa
 }
 
 constexpr int kPass = 128;        // outputs per pass
-constexpr int kRowF = kPass + 4;  // a tile row in LDS, in floats: 16 rows start in 16 different bank groups
 
-// 8 ranks from 8 r8 on of one row's t to LDS: [ranks / 32][terms][`bytes` of rows of 32].
+// 8 ranks from 8 r8 on of one row's t to LDS: [ranks / 32][kTerms][`bytes` of rows of 32].
 __device__ __forceinline__ void put_t(const Lora& p, int64_t m, int row, int r8, int rank, float scale, uint8_t* s_t,
-                                      int bytes, int terms) {
+                                      int bytes) {
     f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     const float* src = p.part + m * p.ldt + 8 * r8;
 #pragma unroll 8
@@ -408,8 +408,9 @@ __device__ __forceinline__ void put_t(const Lora& p, int64_t m, int row, int r8,
     float t[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) t[e] = 8 * r8 + e < rank ? scale * v[e >> 2][e & 3] : 0.f;
-    uint8_t* dst = s_t + (r8 >> 2) * (terms * bytes) + row * 64 + 16 * (r8 & 3);
-    for (int term = 0; term < terms; ++term) {
+    uint8_t* dst = s_t + (r8 >> 2) * (kTerms * bytes) + row * 64 + 16 * (r8 & 3);
+#pragma unroll
+    for (int term = 0; term < kTerms; ++term) {
         u32x4 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -449,12 +450,13 @@ __device__ __forceinline__ void cut_b(int have, u32x4 (&b)[J]) {
     }
 }
 
-// Outputs [n, n + cnt) of a row from its sums in LDS (NULL: none) and base.
+// Outputs [n, n + cnt) of a row from its sums in LDS (four each at a and b; NULL: none) and base.
 template <int BASE>
-__device__ __forceinline__ void finish8(void* y, int y_f32, const float* sums, const Base8<BASE>& base, uint32_t at, int cnt) {
+__device__ __forceinline__ void finish8(void* y, int y_f32, const f32x4* a_at, const f32x4* b_at, const Base8<BASE>& base,
+                                        uint32_t at, int cnt) {
     float o[8];
-    if (sums) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(sums), b = *reinterpret_cast<const f32x4*>(sums + 4);
+    if (a_at) {
+        const f32x4 a = *a_at, b = *b_at;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = (e < 4 ? a[e & 3] : b[e & 3]) + base.at(e);
     } else {
@@ -464,18 +466,25 @@ __device__ __forceinline__ void finish8(void* y, int y_f32, const float* sums, c
     store8(y, y_f32, at, o, cnt);
 }
 
+// The tile of sums in LDS: rows of kPass floats, four outputs (`quad`, of kPass / 4) apiece, XOR-swizzled so
+// that 16 rows' pieces of one quad lie in 16 different bank groups (without padding: with it two workgroups of
+// rank 128 would not fit a CU).
+__device__ __forceinline__ f32x4* sums_at(uint8_t* s_d, int row, int quad) {
+    return reinterpret_cast<f32x4*>(s_d + kPass * 4 * row + 16 * (quad ^ (row & 15)));
+}
+
 // Few rows.  Wave job: (row, pass of outputs), the rows of few_rows.  Waves are
 // independent of each other.
 constexpr int kFewBytes = 16 * 64;             // of one term of 32 ranks of 16 rows' t
-constexpr int kFewTile = 16 * kRowF * 4;
+constexpr int kFewTile = 16 * kPass * 4;
 
 template <int BASE>
 __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int passes) {
     extern __shared__ __attribute__((aligned(16))) uint8_t s_all[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane >> 4, col = lane & 15, N = (int)p.a.rows, t_bytes = (p.ldt + 31) / 32 * p.terms * kFewBytes;
-    uint8_t* s_t = s_all + wave * (kFewTile + t_bytes);        // [ranks / 32][terms][16][32] bf16
-    float* s_d = reinterpret_cast<float*>(s_t + t_bytes);      // [16][kRowF]
+    const int q = lane >> 4, col = lane & 15, N = (int)p.a.rows, t_bytes = (p.ldt + 31) / 32 * kTerms * kFewBytes;
+    uint8_t* s_t = s_all + wave * (kFewTile + t_bytes);        // [ranks / 32][kTerms][16][32] bf16
+    uint8_t* s_d = s_t + t_bytes;                              // 16 rows of sums
     const int64_t job = (int64_t)blockIdx.x * kWaves + wave;
     if (job >= p.M * passes) return;
     const int n0 = (int)(job % passes) * kPass, n_hi = min(N, n0 + kPass);
@@ -499,7 +508,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int
         for (int w0 = 0; w0 < f.n * groups; w0 += 64) {
             const int w = w0 + lane, r = w / groups, r8 = w - r * groups;
             const int64_t m = __shfl((int)f.m, r & 15, 64);  // ahead of the condition: from lanes that may not meet it
-            if (r < f.n) put_t(p, m, r, r8, rank, scale, s_t, kFewBytes, p.terms);
+            if (r < f.n) put_t(p, m, r, r8, rank, scale, s_t, kFewBytes);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -512,39 +521,42 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int
                 u32x4 b[4];
                 load_b<4>(B, p.a.ld_B, n0 + 64 * half, N, have, kb, b);
                 cut_b<4>(have, b);
-                for (int term = p.terms - 1; term >= 0; --term) {
+#pragma unroll
+                for (int term = kTerms - 1; term >= 0; --term) {
                     u32x4 t = {0u, 0u, 0u, 0u};
                     if (have > 0)
-                        t = *reinterpret_cast<const u32x4*>(s_t + (kb * p.terms + term) * kFewBytes + col * 64 + 16 * q);
+                        t = *reinterpret_cast<const u32x4*>(s_t + (kb * kTerms + term) * kFewBytes + col * 64 + 16 * q);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[j] = mfma(b[j], t, acc[j]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // D: row col of the job, outputs 16 j + 4 q .. + 3
-                *reinterpret_cast<f32x4*>(s_d + col * kRowF + 64 * half + 16 * j + 4 * q) = acc[j];
+                *sums_at(s_d, col, 16 * half + 4 * j + q) = acc[j];
         }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
         if (4 * s + q < f.n && cnt > 0)
-            finish8<BASE>(static_cast<char*>(p.y) + at[s] * (p.y_f32 ? 4 : 2), p.y_f32, f.idx >= 0 ? s_d + (4 * s + q) * kRowF + 8 * col : nullptr, base[s], (uint32_t)n, cnt);
+            finish8<BASE>(static_cast<char*>(p.y) + at[s] * (p.y_f32 ? 4 : 2), p.y_f32,
+                          f.idx >= 0 ? sums_at(s_d, 4 * s + q, 2 * col) : nullptr, sums_at(s_d, 4 * s + q, 2 * col + 1), base[s],
+                          (uint32_t)n, cnt);
 }
 
 // Many rows.  A workgroup: 64 rows and a range of outputs; in a pass a wave has
 // 32 of the 128 outputs, against all 64 rows.
 constexpr int kManyBytes = 64 * 64;            // of one term of 32 ranks of 64 rows' t
-constexpr int kManyTile = 64 * kRowF * 4;
+constexpr int kManyTile = 64 * kPass * 4;
 
 // Three workgroups a CU (168 registers) where base is bf16: 100 us against 121 with two (4096 rows, rank 16,
-// 5120 -> 17408); an fp32 base does not fit them.
-template <int BASE, int TERMS>
+// 5120 -> 17408); an fp32 base does not fit them, and from rank 33 on the rows' t leaves LDS for two.
+template <int BASE>
 __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_expand_blocks(const Lora p, int ranges, int range) {
     extern __shared__ __attribute__((aligned(16))) uint8_t s_all[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, col = lane & 15, N = (int)p.a.rows;
-    float* s_d = reinterpret_cast<float*>(s_all);  // [64][kRowF]
-    uint8_t* s_t = s_all + kManyTile;              // [ranks / 32][terms][64][32] bf16
+    uint8_t* s_d = s_all;              // 64 rows of sums
+    uint8_t* s_t = s_all + kManyTile;  // [ranks / 32][kTerms][64][32] bf16
     const int64_t m0 = (int64_t)(blockIdx.x / ranges) * 64;
     const int n_lo = blockIdx.x % ranges * range, n_hi = min(N, n_lo + range);
     const char* base_0 = static_cast<const char*>(p.base) + m0 * N * (BASE == kBaseF32 ? 4 : 2);
@@ -570,7 +582,7 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
     for (int w = tid; w < 64 * groups; w += 64 * kWaves) {
         const int r = w / groups, r8 = w - r * groups, rank_r = __shfl(rank, r, 64);
         const float scale_r = __shfl(scale, r, 64);
-        if (8 * r8 < rank_r) put_t(p, m0 + r, r, r8, rank_r, scale_r, s_t, kManyBytes, TERMS);
+        if (8 * r8 < rank_r) put_t(p, m0 + r, r, r8, rank_r, scale_r, s_t, kManyBytes);
     }
     int row_idx[4];
 #pragma unroll
@@ -613,15 +625,15 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (!(rows >> (16 * t) & 0xFFFFu)) continue;  // uniform
-                    const uint8_t* at = s_t + kb * (TERMS * kManyBytes) + (16 * t + col) * 64 + 16 * q;
-                    u32x4 tv[TERMS];
+                    const uint8_t* at = s_t + kb * (kTerms * kManyBytes) + (16 * t + col) * 64 + 16 * q;
+                    u32x4 tv[kTerms];
 #pragma unroll
-                    for (int u = 0; u < TERMS; ++u) {
+                    for (int u = 0; u < kTerms; ++u) {
                         tv[u] = u32x4{0u, 0u, 0u, 0u};
                         if (have > 0) tv[u] = *reinterpret_cast<const u32x4*>(at + u * kManyBytes);
                     }
 #pragma unroll
-                    for (int u = TERMS - 1; u >= 0; --u)
+                    for (int u = kTerms - 1; u >= 0; --u)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) acc[t][j] = mfma(b[j], tv[u], acc[t][j]);
                 }
@@ -631,7 +643,7 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
                 if (row_idx[t] == i) {  // D: row 16 t + col of the block, outputs 16 j + 4 q .. + 3
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<f32x4*>(s_d + (16 * t + col) * kRowF + 32 * wave + 16 * j + 4 * q) = acc[t][j];
+                        *sums_at(s_d, 16 * t + col, 8 * wave + 4 * j + q) = acc[t][j];
                 }
         }
         if (n0 + kPass < n_hi) {
@@ -644,7 +656,8 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * s + g;
             if ((there >> r & 1) && n < n_hi)
-                finish8<BASE>(y_0, p.y_f32, with >> r & 1 ? s_d + r * kRowF + 8 * col : nullptr, now[s], (uint32_t)(r * N + n), min(8, n_hi - n));
+                finish8<BASE>(y_0, p.y_f32, with >> r & 1 ? sums_at(s_d, r, 2 * col) : nullptr, sums_at(s_d, r, 2 * col + 1),
+                              now[s], (uint32_t)(r * N + n), min(8, n_hi - n));
         }
         lds_barrier();  // the tile is read
     };
@@ -694,7 +707,7 @@ hipError_t launch_base(const Lora& p, const LoraPlan& pl, hipStream_t s) {
         const int64_t grid = (p.M * passes + kWaves - 1) / kWaves;
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
         hipLaunchKernelGGL(lora_expand_few<BASE>, dim3((unsigned)grid), dim3(64 * kWaves),
-                           (size_t)(kblocks * p.terms * kFewBytes + kFewTile) * kWaves, s, p, passes);
+                           (size_t)(kblocks * kTerms * kFewBytes + kFewTile) * kWaves, s, p, passes);
     } else {
         // up to four passes share the rows' t (4096 rows, rank 64, 8 / 4 / 2 passes: 148 / 130 / 132 us),
         // as long as there are 1024 workgroups
@@ -702,8 +715,8 @@ hipError_t launch_base(const Lora& p, const LoraPlan& pl, hipStream_t s) {
         const int ranges = (N + range - 1) / range;
         const int64_t grid = pl.blocks * ranges;
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((p.terms == 2 ? lora_expand_blocks<BASE, 2> : lora_expand_blocks<BASE, 3>), dim3((unsigned)grid),
-                           dim3(64 * kWaves), (size_t)(kblocks * p.terms * kManyBytes + kManyTile), s, p, ranges, range);
+        hipLaunchKernelGGL(lora_expand_blocks<BASE>, dim3((unsigned)grid), dim3(64 * kWaves),
+                           (size_t)(kblocks * kTerms * kManyBytes + kManyTile), s, p, ranges, range);
     }
     return hipGetLastError();
 }
@@ -729,7 +742,7 @@ size_t lora_workspace(const fqm_adapters& a, int64_t M) {
 hipError_t launch_lora(const fqm_adapters& a, const uint16_t* x, const int32_t* index, const void* base,
                        int base_f32, void* y, int y_f32, int64_t M, float* ws, hipStream_t s) {
     const LoraPlan pl = lora_plan(a, M);
-    const Lora p = {a, x, index, base, y, y_f32, M, ws, pl.ldt, pl.ksplit, y_f32 ? 3 : 2};
+    const Lora p = {a, x, index, base, y, y_f32, M, ws, pl.ldt, pl.ksplit};
     const hipError_t e = pl.rb == 1   ? launch_shrink<1>(p, pl, s)
                          : pl.rb == 2 ? launch_shrink<2>(p, pl, s)
                                       : launch_shrink<4>(p, pl, s);

@@ -1,0 +1,56 @@
+"""What the adapters' second product keeps of t = scale * (A x): every bit of
+the fp32 value, whatever type y has, in both forms of the call (rows collected
+from a small batch, blocks of 64 rows of a large one)."""
+import numpy as np
+import pytest
+import torch
+
+import dequant_matmul_amd as fqm
+import oracle
+import synth
+from gpu_common import DEV, bf16_dev, to_f64
+from test_gpu_lora import T, order, pool, want
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("base", [None, "bf16", "f32"])
+@pytest.mark.parametrize("M,count,rank,K,N,kind,mixed", [
+    (1, 4, 16, 1024, 4096, "one", False),
+    (48, 9, 32, 2048, 1000, "any", True),
+    (200, 5, 100, 520, 257, "runs", True),
+    (300, 6, 64, 1024, 640, "runs", False),
+    (513, 3, 24, 328, 1025, "any", True),
+])
+def test_a_bf16_output_is_the_fp32_one_rounded(M, count, rank, K, N, kind, mixed, base):
+    """The type of y decides its last rounding and nothing else."""
+    print(f"lora bf16 and f32 M {M} count {count} rank {rank} {K}->{N} {kind} {base}", flush=True)
+    rng = np.random.default_rng([M, rank, K])
+    ad, _ = pool(count, rank, K, N, seed=M, mixed=mixed)
+    x = bf16_dev(synth.activations(M, K, 5))
+    index = torch.from_numpy(order(kind, M, count, rng).astype(np.int32)).to(DEV)
+    b = torch.from_numpy(rng.standard_normal((M, N))).to(DEV).to(T[base]) if base else None
+    fine = fqm.lora(ad, x, index, base=b, out_dtype=torch.float32)
+    y = fqm.lora(ad, x, index, base=b, out_dtype=torch.bfloat16)
+    assert torch.equal(y, fine.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [4, 300])
+def test_all_24_bits_of_t_reach_y(M, out):
+    """t = 1 + 2^-12 + 2^-23 (or its negative): three products of eight bits and less, exact in fp32, and so are its
+    products with powers of two.  Two bf16 terms of it would lose the last one."""
+    K, N = 64, 140
+    A = torch.zeros(1, 2, K, dtype=torch.bfloat16, device=DEV)
+    A[0, 0, 0], A[0, 0, 1], A[0, 0, 2] = 1.0, 2.0 ** -12, 2.0 ** -23
+    A[0, 1] = -A[0, 0]
+    B = torch.zeros(1, N, 2, dtype=torch.bfloat16, device=DEV)
+    B[0, ::2, 0], B[0, 1::2, 1] = 4.0, 0.5
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[:, :3] = 1.0
+    index = torch.zeros(M, dtype=torch.int32, device=DEV)
+    # the base takes all but t's last bit away
+    base = torch.zeros(M, N, device=DEV)
+    base[:, ::2], base[:, 1::2] = -4 * (1 + 2.0 ** -12), 0.5 * (1 + 2.0 ** -12)
+    y = fqm.lora(fqm.Adapters(A, B), x, index, base=base, out_dtype=T[out])
+    assert (y[:, ::2] == 2.0 ** -21).all() and (y[:, 1::2] == -(2.0 ** -24)).all()
