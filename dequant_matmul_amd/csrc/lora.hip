@@ -312,11 +312,12 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_blocks(const Lora p, 
 }
 
 // ---- y = base + B t ---------------------------------------------------------------
-// The rows' t = scale * (sum of the K parts) goes to LDS as bf16 terms, t_0 =
-// bf16(t), t_1 = bf16(t - t_0), t_2 = bf16(t - t_0 - t_1), each against the same
-// B, smallest first.  The products are exact in fp32, and the three terms are t
-// to 2^-25 of it, whatever y's type (two terms would leave 2^-17, enough to turn
-// the rounding of some bf16 outputs).  In a pass of 128 outputs every distinct
+// The rows' t = scale * (sum of the K parts) goes to LDS as three bf16 terms, each
+// the leading 8 bits of what the ones before it leave, cut off, not rounded (the
+// largest fp32 values would round up to infinity): 24 bits, all of t, whatever
+// y's type (two terms would leave 2^-16, enough to turn the rounding of some bf16
+// outputs).  Each meets the same B, smallest first, and the products are exact
+// in fp32.  In a pass of 128 outputs every distinct
 // adapter's B meets the block's rows and its own rows' sums go to a tile in LDS;
 // then base streams through it to y in whole lines, the next pass's base already
 // requested.  (Straight from the matrix layout, 16 rows a load, the same took 1.5
@@ -418,11 +419,11 @@ __device__ __forceinline__ void put_t(const Lora& p, int64_t m, int row, int r8,
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float& left = t[2 * e + c];
-                h[c] = bf16_bits(left);
+                h[c] = __float_as_uint(left) & 0xFFFF0000u;
                 // an infinite t has one term (inf - inf is none)
-                left = (h[c] & 0x7F80u) == 0x7F80u ? 0.f : left - bf16_to_f32(h[c]);
+                left = (h[c] & 0x7F800000u) == 0x7F800000u ? 0.f : left - __uint_as_float(h[c]);
             }
-            o[e] = h[0] | h[1] << 16;
+            o[e] = h[0] >> 16 | h[1];
         }
         *reinterpret_cast<u32x4*>(dst + term * bytes) = o;
     }

@@ -392,8 +392,8 @@ size_t fqm_lora_workspace_size(const fqm_adapters* a, int64_t M);
  * and y need only their element's alignment and may be the same buffer
  * (then of the same dtype); no other buffers may overlap.
  * A x is kept in fp32; B_i (A_i x) is formed on the matrix cores from scale * A x
- * as a sum of three bf16 terms, exact to 2^-25 of it; a bf16 y is the fp32 y
- * rounded once.  workspace as for fqm_gemv.  Results do not depend on timing, nor on
+ * as a sum of three bf16 terms, exact (below 2^-100: to 2^-125); a bf16 y is the
+ * fp32 y rounded once.  workspace as for fqm_gemv.  Results do not depend on timing, nor on
  * the other rows' values. */
 fqm_status fqm_lora(const fqm_adapters* a, const uint16_t* x, const int32_t* index, const void* base,
                     int32_t base_dtype, void* y, int32_t y_dtype, int64_t M, void* workspace,

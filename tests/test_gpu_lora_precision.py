@@ -54,3 +54,20 @@ def test_all_24_bits_of_t_reach_y(M, out):
     base[:, ::2], base[:, 1::2] = -4 * (1 + 2.0 ** -12), 0.5 * (1 + 2.0 ** -12)
     y = fqm.lora(fqm.Adapters(A, B), x, index, base=base, out_dtype=T[out])
     assert (y[:, ::2] == 2.0 ** -21).all() and (y[:, 1::2] == -(2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_a_t_near_the_largest_fp32_stays_finite(M):
+    """t between bf16's largest value and fp32's: its leading bf16 term must not round up to infinity."""
+    K, N = 64, 70
+    A = torch.zeros(1, 2, K, dtype=torch.bfloat16, device=DEV)
+    A[0, 0, 0], A[0, 1, 0] = 2.0 ** 127, -(2.0 ** 127)
+    B = torch.full((1, N, 2), 0.0, dtype=torch.bfloat16, device=DEV)
+    B[0, ::2, 0], B[0, 1::2, 1] = 2.0 ** -100, 2.0 ** -100
+    scale = torch.tensor([1.99951171875], device=DEV)  # 2 - 2^-11: t = +-2^127 (2 - 2^-11), exact in fp32
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = 1.0
+    index = torch.zeros(M, dtype=torch.int32, device=DEV)
+    y = fqm.lora(fqm.Adapters(A, B, scale), x, index, out_dtype=torch.float32)
+    t = 2.0 ** 27 * 1.99951171875  # one product, exact
+    assert (y[:, ::2] == t).all() and (y[:, 1::2] == -t).all()
