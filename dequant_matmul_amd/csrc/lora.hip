@@ -317,11 +317,11 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_blocks(const Lora p, 
 // largest fp32 values would round up to infinity): 24 bits, all of t, whatever
 // y's type (two terms would leave 2^-16, enough to turn the rounding of some bf16
 // outputs).  Each meets the same B, smallest first, and the products are exact
-// in fp32.  In a pass of 128 outputs every distinct
-// adapter's B meets the block's rows and its own rows' sums go to a tile in LDS;
-// then base streams through it to y in whole lines, the next pass's base already
-// requested.  (Straight from the matrix layout, 16 rows a load, the same took 1.5
-// to 2 times as long with many rows.)
+// in fp32; where B is not finite only the leading term meets it (finite_of).  In
+// a pass of 128 outputs every distinct adapter's B meets the block's rows and its
+// own rows' sums go to a tile in LDS; then base streams through it to y in whole
+// lines, the next pass's base already requested.  (Straight from the matrix
+// layout, 16 rows a load, the same took 1.5 to 2 times as long with many rows.)
 constexpr int kTerms = 3;
 
 enum BaseKind { kNoBase = 0, kBaseBf16 = 1, kBaseF32 = 2 };
@@ -467,6 +467,29 @@ __device__ __forceinline__ void finish8(void* y, int y_f32, const f32x4* a_at, c
     store8(y, y_f32, at, o, cnt);
 }
 
+// What t's lower terms meet: B without its infinities and NaN.  A lower term may
+// be zero or of the other sign, and its product with an infinity would turn the
+// leading term's into NaN.  Whether there are any is uniform, and hardly ever true.
+template <int J>
+__device__ __forceinline__ void finite_of(const u32x4 (&b)[J], u32x4 (&low)[J]) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= (b[j][e] & 0x7F807F80u) + 0x00800080u;  // bit 15 / 31: the half's exponent is full
+#pragma unroll
+    for (int j = 0; j < J; ++j) low[j] = b[j];
+    if (__builtin_expect(__ballot((any & 0x80008000u) != 0) != 0, 0)) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t full = ((b[j][e] & 0x7F807F80u) + 0x00800080u) >> 15 & 0x00010001u;
+                low[j][e] &= ~((full << 16) - full);
+            }
+    }
+}
+
 // The tile of sums in LDS: rows of kPass floats, four outputs (`quad`, of kPass / 4) apiece, XOR-swizzled so
 // that 16 rows' pieces of one quad lie in 16 different bank groups (without padding: with it two workgroups of
 // rank 128 would not fit a CU).
@@ -522,13 +545,15 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int
                 u32x4 b[4];
                 load_b<4>(B, p.a.ld_B, n0 + 64 * half, N, have, kb, b);
                 cut_b<4>(have, b);
+                u32x4 low[4];
+                finite_of<4>(b, low);
 #pragma unroll
                 for (int term = kTerms - 1; term >= 0; --term) {
                     u32x4 t = {0u, 0u, 0u, 0u};
                     if (have > 0)
                         t = *reinterpret_cast<const u32x4*>(s_t + (kb * kTerms + term) * kFewBytes + col * 64 + 16 * q);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j] = mfma(b[j], t, acc[j]);
+                    for (int j = 0; j < 4; ++j) acc[j] = mfma(term ? low[j] : b[j], t, acc[j]);
                 }
             }
 #pragma unroll
@@ -623,6 +648,8 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
                     load_b<2>(B, p.a.ld_B, nw, N, have, kb, b);
                 }
                 cut_b<2>(have, b);
+                u32x4 low[2];
+                finite_of<2>(b, low);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (!(rows >> (16 * t) & 0xFFFFu)) continue;  // uniform
@@ -636,7 +663,7 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
 #pragma unroll
                     for (int u = kTerms - 1; u >= 0; --u)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[t][j] = mfma(b[j], tv[u], acc[t][j]);
+                        for (int j = 0; j < 2; ++j) acc[t][j] = mfma(u ? low[j] : b[j], tv[u], acc[t][j]);
                 }
             }
 #pragma unroll

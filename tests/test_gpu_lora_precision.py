@@ -71,3 +71,30 @@ def test_a_t_near_the_largest_fp32_stays_finite(M):
     y = fqm.lora(fqm.Adapters(A, B, scale), x, index, out_dtype=torch.float32)
     t = 2.0 ** 27 * 1.99951171875  # one product, exact
     assert (y[:, ::2] == t).all() and (y[:, 1::2] == -t).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("rank", [3, 40, 72])
+def test_infinities_and_nan_of_b_give_what_the_sum_gives(rank, M, out):
+    """Small whole numbers: t and y are exact, and t's lower bf16 terms are zeros, which must not meet an infinity."""
+    K, N, count = 64, 150, 2
+    g = torch.Generator().manual_seed(rank)
+    A = torch.randint(-1, 2, (count, rank, K), generator=g).double()
+    B = torch.randint(-4, 5, (count, N, rank), generator=g).double()
+    inf = float("inf")
+    B[0, 5, 0], B[0, 9, rank - 1], B[0, 64, 1], B[1, 149, 2] = inf, -inf, float("nan"), inf
+    B[0, 17, 0], B[0, 17, 1] = inf, -inf
+    x = torch.randint(-2, 3, (M, K), generator=g).double()
+    index = torch.arange(M, dtype=torch.int32) % 3 - 1 if M > 1 else torch.zeros(1, dtype=torch.int32)
+    base = torch.randint(-8, 9, (M, N), generator=g).double()
+    ad = fqm.Adapters(A.to(torch.bfloat16).to(DEV), B.to(torch.bfloat16).to(DEV))
+    y = fqm.lora(ad, x.to(torch.bfloat16).to(DEV), index.to(DEV), base=base.to(torch.bfloat16).to(DEV), out_dtype=T[out])
+    want_ = base.clone()
+    for m in range(M):
+        i = int(index[m])
+        if i >= 0:
+            want_[m] += (B[i] * (A[i] @ x[m])).sum(1)
+    assert torch.isinf(want_).any() and torch.isnan(want_).any()
+    assert torch.equal(torch.nan_to_num(y.cpu().float(), nan=1e30, posinf=2e30, neginf=-2e30),
+                       torch.nan_to_num(want_.to(T[out]).float(), nan=1e30, posinf=2e30, neginf=-2e30))
