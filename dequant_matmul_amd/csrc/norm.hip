@@ -252,7 +252,8 @@ __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_nor
     }
     const int64_t yr = row * a.ld_y;
     if (a.y_dtype == FQM_I8) {
-        const float scale = r * mx / 127.f;
+        // a row of zeros has scale 0 with eps = 0 too, where r is infinite (a NaN in the row is in sq)
+        const float scale = sq == 0.f && mx == 0.f ? 0.f : r * mx / 127.f;
         // codes: y / scale; 0 where the scale is 0, infinite or NaN (its own arithmetic decides, so that
         // the codes are 0 exactly where the stored scale cannot be used)
         const bool use = scale > 0.f && scale <= 3.4e38f;
