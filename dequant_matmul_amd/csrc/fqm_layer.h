@@ -15,6 +15,15 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Between LDS writes of a wave's lanes and reads of the same places by its other
+// lanes: a wave's LDS operations are in order, this makes the compiler keep them
+// so (no instruction).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 hipError_t launch_add_rms_norm(const fqm_norm& a, hipStream_t s);
 
 size_t lora_workspace(const fqm_adapters& a, int64_t M);

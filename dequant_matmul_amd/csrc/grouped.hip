@@ -315,7 +315,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void grouped_rows_kernel(const Grou
         else if (nrows == 2) dot_rows<BITS, 2>(W, R, tab, xs, stride, pieces, cr, s_sum[wave]);
         else if (nrows == 3) dot_rows<BITS, 3>(W, R, tab, xs, stride, pieces, cr, s_sum[wave]);
         else dot_rows<BITS, 4>(W, R, tab, xs, stride, pieces, cr, s_sum[wave]);
-        // lane (r, b) of the wave stores row r of W, row b of X (LDS operations of a wave are in order)
+        wave_lds_order();
+        // lane (r, b) of the wave stores row r of W, row b of X
         const int b = lane % kMaxB, r = lane / kMaxB;
         if (r < R && b < nrows) {
             const int i = i0 + b, n = W.number(r), yr = y_row(g, i);

@@ -534,6 +534,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int
             const int64_t m = __shfl((int)f.m, r & 15, 64);  // ahead of the condition: from lanes that may not meet it
             if (r < f.n) put_t(p, m, r, r8, rank, scale, s_t, kFewBytes);
         }
+        wave_lds_order();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             if (n0 + 64 * half >= n_hi) break;
@@ -560,6 +561,7 @@ __global__ __launch_bounds__(64 * kWaves) void lora_expand_few(const Lora p, int
             for (int j = 0; j < 4; ++j)  // D: row col of the job, outputs 16 j + 4 q .. + 3
                 *sums_at(s_d, col, 16 * half + 4 * j + q) = acc[j];
         }
+        wave_lds_order();
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
