@@ -282,8 +282,8 @@ def lora(adapters: Adapters, x: torch.Tensor, index: torch.Tensor, base: torch.T
 # ---------------------------------------------------------------------------
 # products grouped by expert
 # ---------------------------------------------------------------------------
-def _groups(w: _WeightsBase, X, offsets, src, x_scale, dst, row_scale, Y, out_dtype, y_rows):
-    """Checks the operands; returns the descriptor and Y."""
+def _groups(w: _WeightsBase, X, offsets, src, x_scale, dst, row_scale, Y, out_dtype, y_rows, sizes_only=False):
+    """Checks the operands; returns the descriptor and Y (sizes_only: a descriptor without Y)."""
     if getattr(w, "fmt", None) not in (FQM_LUT6, FQM_LUT4):
         raise ValueError("grouped products take Lut6Weights or Lut4Weights")
     dev = w.packed.device
@@ -308,16 +308,18 @@ def _groups(w: _WeightsBase, X, offsets, src, x_scale, dst, row_scale, Y, out_dt
     if Y is None:
         if out_dtype not in _VALUE:
             raise ValueError(f"out_dtype must be bfloat16 or float32, not {out_dtype}")
-        Y = torch.empty((y_rows, rows), dtype=out_dtype, device=dev)
+        if not sizes_only:
+            Y = torch.empty((y_rows, rows), dtype=out_dtype, device=dev)
     else:
         _need(Y, "Y", _VALUE, dev)
-    if tuple(Y.shape) != (y_rows, rows) or not Y.is_contiguous():
-        raise ValueError(f"Y has shape {tuple(Y.shape)}; expected contiguous ({y_rows}, {rows})")
+        out_dtype = Y.dtype
+        if tuple(Y.shape) != (y_rows, rows) or not Y.is_contiguous():
+            raise ValueError(f"Y has shape {tuple(Y.shape)}; expected contiguous ({y_rows}, {rows})")
     if dst is None and y_rows < M:
         raise ValueError(f"Y has {y_rows} rows for {M} grouped rows")
     g = _Groups(count, offsets.data_ptr(), M, X.data_ptr(), _CODE[X.dtype], X.shape[0],
                 _vector(x_scale, "x_scale", X.shape[0], (torch.float32,), dev),
-                _vector(src, "src", M, (torch.int32,), dev), Y.data_ptr(), _CODE[Y.dtype], y_rows,
+                _vector(src, "src", M, (torch.int32,), dev), None if Y is None else Y.data_ptr(), _CODE[out_dtype], y_rows,
                 _vector(dst, "dst", M, (torch.int32,), dev),
                 _vector(row_scale, "row_scale", M, (torch.float32,), dev))
     return g, Y
@@ -327,9 +329,7 @@ def gemm_grouped_workspace_size(w: _WeightsBase, X: torch.Tensor, offsets: torch
                                 src: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
                                 out_dtype: torch.dtype = torch.bfloat16) -> int:
     """Bytes of workspace that gemm_grouped needs for such operands on this device."""
-    M = X.shape[0] if src is None else src.shape[0]
-    Y = torch.empty((M, w.rows // max(1, offsets.shape[0] - 1)), dtype=out_dtype, device=X.device)
-    g, _ = _groups(w, X, offsets, src, x_scale, None, None, Y, out_dtype, None)
+    g, _ = _groups(w, X, offsets, src, x_scale, None, None, None, out_dtype, None, sizes_only=True)
     return int(load().fqm_gemm_grouped_workspace_size(w.ref, ctypes.byref(g)))
 
 

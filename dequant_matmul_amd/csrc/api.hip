@@ -515,7 +515,8 @@ fqm_status check_adapters(const fqm_adapters* a) {
     return FQM_OK;
 }
 
-fqm_status check_groups(const fqm_weights* w, const fqm_groups* g) {
+// What the workspace depends on: sizes and types, no pointer of g.
+fqm_status check_group_sizes(const fqm_weights* w, const fqm_groups* g) {
     const fqm_status st = check_weights(w);
     if (st != FQM_OK) return st;
     if (!lut_format(*w)) return FQM_E_UNSUPPORTED;
@@ -528,6 +529,12 @@ fqm_status check_groups(const fqm_weights* w, const fqm_groups* g) {
     if (g->M == 0 || w->rows == 0) return FQM_OK;
     if ((!g->src && g->x_rows < g->M) || (!g->dst && g->y_rows < g->M)) return FQM_E_SHAPE;
     if (g->src && g->x_rows * w->cols * 2 > INT32_MAX) return FQM_E_SHAPE;
+    return FQM_OK;
+}
+
+fqm_status check_groups(const fqm_weights* w, const fqm_groups* g) {
+    const fqm_status st = check_group_sizes(w, g);
+    if (st != FQM_OK || g->M == 0 || w->rows == 0) return st;
     const bool has_x = g->x_rows > 0 && w->cols > 0;
     if (!g->offsets || (g->y_rows > 0 && !g->Y) || (has_x && !g->X) ||
         (g->x_dtype == FQM_I8 && has_x && !g->x_scale))
@@ -599,7 +606,7 @@ fqm_status fqm_lora(const fqm_adapters* a, const uint16_t* x, const int32_t* ind
 }
 
 size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g) {
-    if (check_groups(w, g) != FQM_OK || g->M == 0 || w->rows == 0) return 0;
+    if (check_group_sizes(w, g) != FQM_OK || g->M == 0 || w->rows == 0) return 0;
     return fqm::grouped_workspace(*w, *g);
 }
 

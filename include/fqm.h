@@ -423,7 +423,8 @@ typedef struct fqm_groups {
 } fqm_groups;
 
 /* Bytes of device workspace fqm_gemm_grouped needs on the current device (a
- * function of the sizes and types only, not of the offsets); 0 for invalid
+ * function of the sizes and types only, and of whether src and dst are there;
+ * g's other pointers are not looked at and may still be NULL); 0 for invalid
  * arguments. */
 size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g);
 

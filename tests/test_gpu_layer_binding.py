@@ -1,0 +1,33 @@
+"""The binding of the operators around the products: what its calls allocate, take and refuse."""
+import numpy as np
+import pytest
+import torch
+
+import dequant_matmul_amd as fqm
+from gpu_common import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def experts(E, N, K):
+    codes = torch.randint(0, 64, (E * N, K), dtype=torch.uint8, device=DEV)
+    return fqm.Lut6Weights.from_codes(codes, np.zeros((E * N, 64), dtype=np.int16), device=DEV)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "i8"])
+def test_asking_for_the_workspace_allocates_nothing(xt):
+    w = experts(4, 512, 256)
+    X = torch.zeros(2000, 256, dtype=torch.int8 if xt == "i8" else torch.bfloat16, device=DEV)
+    xs = torch.ones(2000, device=DEV) if xt == "i8" else None
+    off = torch.tensor([0, 500, 900, 900, 2000], dtype=torch.int32, device=DEV)
+    src = torch.zeros(3000, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    sizes = [fqm.gemm_grouped_workspace_size(w, X, off, x_scale=xs),
+             fqm.gemm_grouped_workspace_size(w, X, off, src=src, x_scale=xs, out_dtype=torch.float32)]
+    assert torch.cuda.max_memory_allocated() == before
+    # and they are enough for the calls they were asked for
+    for need, s, dt in zip(sizes, (None, src), (torch.bfloat16, torch.float32)):
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+        assert fqm.gemm_grouped(w, X, off, src=s, x_scale=xs, out_dtype=dt, workspace=ws).dtype == dt
