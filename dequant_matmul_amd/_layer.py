@@ -201,6 +201,8 @@ class Adapters:
 
     @staticmethod
     def _ld(t):
+        if t.shape[2] == 0:  # no values: any stride, and torch's own is 1
+            return 0
         return t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else (t.shape[2] + 7) // 8 * 8
 
     @classmethod

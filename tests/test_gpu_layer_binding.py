@@ -31,3 +31,15 @@ def test_asking_for_the_workspace_allocates_nothing(xt):
     for need, s, dt in zip(sizes, (None, src), (torch.bfloat16, torch.float32)):
         ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
         assert fqm.gemm_grouped(w, X, off, src=s, x_scale=xs, out_dtype=dt, workspace=ws).dtype == dt
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_adapters_without_inputs_add_nothing(M):
+    A = torch.zeros(2, 4, 0, dtype=torch.bfloat16, device=DEV)
+    B = torch.randn(2, 70, 4, device=DEV).to(torch.bfloat16)
+    x = torch.zeros(M, 0, dtype=torch.bfloat16, device=DEV)
+    index = torch.arange(M, dtype=torch.int32, device=DEV) % 3 - 1
+    base = torch.randn(M, 70, device=DEV)
+    ad = fqm.Adapters(A, B)
+    assert torch.equal(fqm.lora(ad, x, index, base=base, out_dtype=torch.float32), base)
+    assert (fqm.lora(ad, x, index) == 0).all()
