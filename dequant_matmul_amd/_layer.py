@@ -175,9 +175,11 @@ class Adapters:
 
     scale: [count] fp32 (ones if None).  ranks: [count] int32 where adapters
     have ranks below the layout's; what A and B hold past them is not used.
-    A's and B's last dimension must be dense with row strides that are
-    multiples of 8 values and matrices back to back; a B of another layout
-    (a rank that is no multiple of 8, for one) is copied into padded rows."""
+    A and B are read in place where their last dimension is dense with row
+    strides that are multiples of 8 values, their matrices lie back to back and
+    they start at a multiple of 16 bytes; others (a rank that is no multiple of
+    8, for one) are copied into padded rows, and what is written to them later
+    does not reach the copy."""
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None = None,
                  ranks: torch.Tensor | None = None):
@@ -192,7 +194,7 @@ class Adapters:
             raise ValueError(f"{self.count} adapters of rank {self.rank}: 1 to 65536, ranks 1 to 256")
         if self.cols % 8:
             raise ValueError(f"{self.cols} inputs: a multiple of 8 is needed")
-        self.A, self.B = A.contiguous() if not self._rows_fit(A) else A, B if self._rows_fit(B) else self._padded(B)
+        self.A, self.B = (t if self._rows_fit(t) else self._padded(t) for t in (A, B))
         self.scale, self.ranks = scale, ranks
         self.desc = _Adapters(self.count, self.rank, self.rows, self.cols, self.A.data_ptr(), self._ld(self.A),
                               self.B.data_ptr(), self._ld(self.B),

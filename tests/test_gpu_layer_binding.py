@@ -43,3 +43,13 @@ def test_adapters_without_inputs_add_nothing(M):
     ad = fqm.Adapters(A, B)
     assert torch.equal(fqm.lora(ad, x, index, base=base, out_dtype=torch.float32), base)
     assert (fqm.lora(ad, x, index) == 0).all()
+
+
+def test_adapters_at_any_address():
+    flat = torch.randn(3 * 8 * 256 + 8, device=DEV).to(torch.bfloat16)
+    A = flat[3:3 + 3 * 8 * 256].view(3, 8, 256)
+    B = torch.randn(3 * 70 * 8 + 8, device=DEV).to(torch.bfloat16)[5:5 + 3 * 70 * 8].view(3, 70, 8)
+    assert A.data_ptr() % 16 and B.data_ptr() % 16
+    x = torch.randn(4, 256, device=DEV).to(torch.bfloat16)
+    index = torch.tensor([2, 0, -1, 1], dtype=torch.int32, device=DEV)
+    assert torch.equal(fqm.lora(fqm.Adapters(A, B), x, index), fqm.lora(fqm.Adapters(A.clone(), B.clone()), x, index))
