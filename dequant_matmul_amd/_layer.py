@@ -307,6 +307,8 @@ def _groups(w: _WeightsBase, X, offsets, src, x_scale, dst, row_scale, Y, out_dt
     if src is not None:
         _need(src, "src", (torch.int32,), dev, dim=1)
         M = src.shape[0]
+    if Y is not None:
+        _need(Y, "Y", _VALUE, dev, dim=2)
     if y_rows is None:
         y_rows = M if Y is None else Y.shape[0]
     if Y is None:
@@ -315,7 +317,6 @@ def _groups(w: _WeightsBase, X, offsets, src, x_scale, dst, row_scale, Y, out_dt
         if not sizes_only:
             Y = torch.empty((y_rows, rows), dtype=out_dtype, device=dev)
     else:
-        _need(Y, "Y", _VALUE, dev)
         out_dtype = Y.dtype
         if tuple(Y.shape) != (y_rows, rows) or not Y.is_contiguous():
             raise ValueError(f"Y has shape {tuple(Y.shape)}; expected contiguous ({y_rows}, {rows})")

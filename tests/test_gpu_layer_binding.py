@@ -53,3 +53,12 @@ def test_adapters_at_any_address():
     x = torch.randn(4, 256, device=DEV).to(torch.bfloat16)
     index = torch.tensor([2, 0, -1, 1], dtype=torch.int32, device=DEV)
     assert torch.equal(fqm.lora(fqm.Adapters(A, B), x, index), fqm.lora(fqm.Adapters(A.clone(), B.clone()), x, index))
+
+
+def test_an_output_that_is_no_matrix_is_refused_like_the_other_operands():
+    w = experts(2, 64, 128)
+    X = torch.zeros(4, 128, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 1, 4], dtype=torch.int32, device=DEV)
+    for Y in ([1.0], torch.tensor(1.0, device=DEV), torch.zeros(4 * 64, device=DEV)):
+        with pytest.raises(ValueError, match="Y "):
+            fqm.gemm_grouped(w, X, off, Y=Y)
