@@ -41,6 +41,8 @@ def _elsewhere(stream, device):
     """Whether the call is for another stream or device than the current ones.  It is then
     made again inside them: what it allocates (outputs, workspace) belongs to that stream,
     so that its memory is not handed out again under the running kernels."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
     return stream is not None or device.index != torch.cuda.current_device()
 
 
