@@ -49,8 +49,8 @@ def lora(A, B, scale, ranks, x, index, base):
     or None (fp64) -> (y, bound).
 
     The products A x: cols terms in fp32; worst case one rounding a term, in
-    chains no longer than cols / 8 + 64.  scale * A x keeps 2^-17 of itself (two
-    bf16 parts, each product exact in fp32), then rank * 2 terms, scale and
+    chains no longer than cols / 8 + 64.  scale * A x is kept whole (three bf16
+    parts, 24 bits, each product exact in fp32), then rank * 3 terms, scale and
     base are added."""
     M, rows = x.shape[0], B.shape[1]
     y = np.zeros((M, rows)) if base is None else base.astype(np.float64).copy()
@@ -63,10 +63,10 @@ def lora(A, B, scale, ranks, x, index, base):
         r = min(max(int(ranks[i]), 0), A.shape[1]) if ranks is not None else A.shape[1]
         s = 1.0 if scale is None else float(scale[i])
         t = A[i, :r] @ x[m]
-        tb = (K / 8 + 64) * U * (np.abs(A[i, :r]) @ np.abs(x[m])) + 2.0 ** -16 * np.abs(t)
+        tb = (K / 8 + 64) * U * (np.abs(A[i, :r]) @ np.abs(x[m]))
         Bi = B[i, :, :r]
         y[m] += s * (Bi @ t)
-        bound[m] += abs(s) * (np.abs(Bi) @ (tb + (2 * r + 8) * U * np.abs(t)))
+        bound[m] += abs(s) * (np.abs(Bi) @ (tb + (3 * r + 8) * U * np.abs(t)))
     return y, bound + 2 * U * np.abs(y)
 
 
