@@ -5,7 +5,8 @@ Argument marshalling only, as in the package's other calls: shapes, types,
 layouts and devices are checked here (the C ABI sees only pointers), the
 computation runs in the HIP kernels behind ``fqm_add_rms_norm``, ``fqm_lora``
 and ``fqm_gemm_grouped`` (include/fqm.h has their definitions).  With ``stream``
-given, what a call allocates belongs to that stream.
+given, what a call allocates belongs to that stream.  There are no gradients, as
+in the package's other calls: outputs are detached from the inputs.
 """
 from __future__ import annotations
 
@@ -246,7 +247,8 @@ def lora(adapters: Adapters, x: torch.Tensor, index: torch.Tensor, base: torch.T
     x [M][cols] bf16; index [M] int32, rows in any order, a value outside
     0..count-1 for a row without an adapter; base [M][rows] bf16 or fp32.
     ``y`` may be ``base`` (the addition in place).  Any M: single tokens and
-    prompts, mixed."""
+    prompts, mixed; above 256 rows the call is 2 to 4 times as fast where each
+    adapter's rows lie together."""
     _need(x, "x", (torch.bfloat16,), adapters.device, dim=2)
     if _elsewhere(stream, x.device):
         with _inside(stream, x.device):

@@ -466,7 +466,8 @@ struct TilePlan {
 // heights 32 / 64 / 128): 64 groups of 6-bit 5120 -> 1024 at 8 rows 81 / 88 / -,
 // 16 rows 114 / 90 / 100, 64 rows 186 / 167 / 158, 256 rows 517 / 377 / 300;
 // 8 groups of 4-bit 5120 -> 2176 at 8 rows 28 / 29 / -, 32 rows 35 / 31 / 46,
-// 96 rows 57 / 50 / 55, 256 rows 116 / 88 / 84.  256-row tiles (one workgroup
+// 96 rows 57 / 50 / 55, 256 rows 116 / 88 / 84.  At its borders the rule costs up
+// to 10 %.  256-row tiles (one workgroup
 // per CU, as the ungrouped product has them) were 0-9 % faster on large even
 // 6-bit groups, 5-40 % slower on ragged and 4-bit ones, and are not built.
 // Splitting K fills the chip when the tiles are few: aimed at 768 workgroups
@@ -517,7 +518,8 @@ int rows_bmax(int64_t K) { return K == 0 ? kMaxB : (int)std::min<int64_t>(kMaxB,
 // 5120 -> 1024 at 1/8 row 14 / 27, 1/2 row 32 / 42, 1 row 55 / 49, 2 rows 87 /
 // 76; 8 groups of 4096 -> 4096 at 1/2 row 14 / 23, 1 row 20 / 26, 2 rows 41 / 32;
 // 40 groups of 2048 -> 1000 at 1/2 row 16 / 21, 1 row 23 / 22; 32 groups of 4-bit
-// 1024 -> 5120 at 1/8 row 11 / 13, 1/4 row 16 / 14, 1/2 row 29 / 17.
+// 1024 -> 5120 at 1/8 row 11 / 13, 1/4 row 16 / 14, 1/2 row 29 / 17.  At its border
+// the rule costs up to 14 %.
 bool rows_path(const fqm_groups& g, int64_t K) {
     return K == 0 || (g.M * 4096 <= g.count * K && rows_bmax(K) >= 1);
 }

@@ -9,12 +9,15 @@
 // products, so a row that is not finite, or another request's adapter,
 // touches no other row.
 //
-// What binds it, on one MI355X: many rows - reading base and writing y (4096 rows,
-// 16 adapters of rank 64, 5120 -> 17408 in bf16: 30 us for the first launch, 100 us
-// for the second, 122 us among other calls, 373 MB at 3.1 TB/s; 17408 -> 5120 115
-// us); few rows - two launches and the latency of the loads in them (1 row, rank
-// 16, 5120 -> 17408: 4.2 + 7.4 us; 48 rows over 32 adapters, 17408 -> 5120: 13 + 9
-// us for 29 MB).
+// What binds it, on one MI355X: many rows - the second launch's loads and their
+// latency (4096 rows, 16 adapters of rank 64, 5120 -> 17408 in bf16: 28 us for the
+// first launch, 130-136 us for the second, 151 us among other calls, 373 MB at
+// 2.5 TB/s; rank 16 91 us, rank 128 182; 17408 -> 5120 of rank 64 106 us).  It
+// reads 308 MB for 180 that it cannot do without: every range of outputs sums the
+// K parts of t again, and a block's B comes to several XCDs; from rank 33 on two
+// workgroups share a CU, not three.  Few rows - two launches and the latency of
+// the loads in them (1 row, rank 16, 5120 -> 17408: 4.2 + 7.2 us; 48 rows over 32
+// adapters, 17408 -> 5120: 12.6 + 7.0 us for 29 MB).
 #include <algorithm>
 
 #include "fqm_layer.h"
@@ -577,7 +580,8 @@ constexpr int kManyBytes = 64 * 64;            // of one term of 32 ranks of 64 
 constexpr int kManyTile = 64 * kPass * 4;
 
 // Three workgroups a CU (168 registers) where base is bf16: 100 us against 121 with two (4096 rows, rank 16,
-// 5120 -> 17408); an fp32 base does not fit them, and from rank 33 on the rows' t leaves LDS for two.
+// 5120 -> 17408; the compiler now stays below 168 by itself, 92 us with this bound or without).  An fp32 base
+// does not fit them, and from rank 33 on the rows' t leaves LDS for two.
 template <int BASE>
 __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_expand_blocks(const Lora p, int ranges, int range) {
     extern __shared__ __attribute__((aligned(16))) uint8_t s_all[];
@@ -701,9 +705,12 @@ __global__ __launch_bounds__(64 * kWaves, BASE == kBaseF32 ? 2 : 3) void lora_ex
 // ---- the plan -----------------------------------------------------------------------
 // Up to kFewRows rows each adapter's rows are collected from the batch; more
 // rows are taken 64 by 64 as they lie.  One MI355X, us for collected / as they
-// lie: 48 rows in any order over 32 adapters (ranks to 32, 17408 -> 5120) 21 /
-// 164, 256 rows 30 / 150; runs of 3 adapters (rank 16, 5120 -> 17408) 128 rows
-// 21 / 16, 512 rows 70 / 27.
+// lie: 48 rows in any order over 32 adapters (ranks to 32, 17408 -> 5120) 19 /
+// 94, 256 rows 29 / 113; runs of 3 adapters (rank 16, 5120 -> 17408) 128 rows
+// 20 / 13, 512 rows 70 / 22.  The rule looks at M alone, so that more than 256 rows
+// in any order are slow: 5120 -> 5120 in bf16, 32 adapters of rank 16, in any order
+// / in runs: 256 rows 18 / 21, 257 rows 70 / 24, 1024 rows 80 / 22; 64 adapters of
+// rank 32: 27 / 31, 101 / 46, 109 / 30.
 constexpr int64_t kFewRows = 256;
 
 struct LoraPlan {
@@ -715,7 +722,7 @@ struct LoraPlan {
 // K parts: as many as fill the chip (512 workgroups of a job's four stretches
 // or 256 of 64-row blocks), each of at least four steps, few enough that adding
 // them up again stays small (4096 rows, rank 64, aimed at 256 / 512 / 768
-// workgroups: 129 / 137 / 143 us).
+// workgroups: 145 / 147 / 161 us).
 LoraPlan lora_plan(const fqm_adapters& a, int64_t M) {
     LoraPlan p;
     p.few = M <= kFewRows;
@@ -739,7 +746,7 @@ hipError_t launch_base(const Lora& p, const LoraPlan& pl, hipStream_t s) {
         hipLaunchKernelGGL(lora_expand_few<BASE>, dim3((unsigned)grid), dim3(64 * kWaves),
                            (size_t)(kblocks * kTerms * kFewBytes + kFewTile) * kWaves, s, p, passes);
     } else {
-        // up to four passes share the rows' t (4096 rows, rank 64, 8 / 4 / 2 passes: 148 / 130 / 132 us),
+        // up to four passes share the rows' t (4096 rows, rank 64, 8 / 4 / 2 passes: 151 / 144 / 150 us),
         // as long as there are 1024 workgroups
         const int range = (int)std::max<int64_t>(1, std::min<int64_t>(4, pl.blocks * passes / 1024)) * kPass;
         const int ranges = (N + range - 1) / range;

@@ -359,6 +359,7 @@ typedef struct fqm_norm {
  * With y_dtype FQM_I8, y_scale[row] = max|y| / 127 and y holds
  * round(y / y_scale) (nearest even, within [-127, 127]); a row of zeros has
  * scale 0 and codes 0; a row whose scale is not finite has codes 0.
+ * mean(h^2) is fp32 too: where h passes about 2^63 it is infinite and y zeros.
  * rows == 0 enqueues nothing; cols == 0 writes zeros to y_scale. */
 fqm_status fqm_add_rms_norm(const fqm_norm* a, void* stream);
 
