@@ -15,8 +15,10 @@ unpacked host arrays and pack them on the GPU with ``fqm_pack_bits``.
 
 Around the products: ``add_rms_norm`` (the residual's addition and the norm in
 front of a product, with an 8-bit form), ``Adapters`` and ``lora`` (low-rank
-adapters of many requests beside a product) and ``gemm_grouped`` (the products
-of many experts, ragged sizes).
+adapters of many requests beside a product), ``route`` (each token's experts and
+the plan of their products) and ``gemm_grouped`` (the products of many experts,
+ragged sizes), ``linear`` (the product with bias, activation and residual in its
+epilogue) and ``block_norm`` (the norms on both sides of a block).
 """
 from __future__ import annotations
 
@@ -32,19 +34,24 @@ LIB_PATH = os.path.join(HERE, "libfqm.so")
 FQM_LUT6, FQM_FABQ, FQM_MDBF, FQM_LUT4 = 1, 2, 3, 4
 FQM_CB_SCALAR16, FQM_CB_TIERED, FQM_CB_VECTOR = 0, 1, 2
 FQM_BF16, FQM_F32, FQM_I8 = 0, 1, 2
+FQM_ACT = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5, "tanh": 6}
+FQM_SCORE = {"softmax": 0, "sigmoid": 1}
+FQM_GROUP_SCORE = {"max": 0, "top2": 1}
 
 __all__ = [
     "FqmError", "FqmNotBuilt", "load", "version", "set_debug", "status_str", "pack_bits", "pack",
     "unpack", "dequant", "workspace_size", "gemv", "gemv_static", "gemm_workspace_size", "gemm", "Lut6Weights", "Lut4Weights", "FabqWeights",
     "MdbfWeights", "SYMBOLS", "add_rms_norm", "NormOut", "Adapters", "lora_workspace_size", "lora",
-    "gemm_grouped_workspace_size", "gemm_grouped",
+    "gemm_grouped_workspace_size", "gemm_grouped", "linear_workspace_size", "linear", "Routing",
+    "route_workspace_size", "route", "block_norm",
 ]
 
 # Every symbol include/fqm.h declares.
 SYMBOLS = ("fqm_version", "fqm_set_debug", "fqm_status_str", "fqm_pack_bits", "fqm_pack", "fqm_unpack",
            "fqm_dequant", "fqm_workspace_size", "fqm_gemv", "fqm_gemv_static",
            "fqm_gemm_workspace_size", "fqm_gemm", "fqm_add_rms_norm", "fqm_lora_workspace_size", "fqm_lora",
-           "fqm_gemm_grouped_workspace_size", "fqm_gemm_grouped")
+           "fqm_gemm_grouped_workspace_size", "fqm_gemm_grouped", "fqm_linear_workspace_size", "fqm_linear",
+           "fqm_route_workspace_size", "fqm_route", "fqm_block_norm")
 STATIC_SCRATCH_BYTES = 16 << 20  # FQM_STATIC_SCRATCH_BYTES
 
 
@@ -115,6 +122,30 @@ class _Groups(ctypes.Structure):
                 ("y_dtype", c_int32), ("y_rows", c_int64), ("dst", c_void_p), ("row_scale", c_void_p)]
 
 
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("X", c_void_p), ("ld_x", c_int64), ("act", c_int32), ("gated", c_int32),
+                ("bias", c_void_p), ("bias_dtype", c_int32), ("res_dtype", c_int32), ("residual", c_void_p),
+                ("ld_res", c_int64), ("Y", c_void_p), ("ld_y", c_int64), ("y_dtype", c_int32)]
+
+
+class _Routing(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("E", c_int32), ("k", c_int32), ("logits", c_void_p), ("ld_x", c_int64),
+                ("x_dtype", c_int32), ("score", c_int32), ("bias", c_void_p), ("groups", c_int32),
+                ("top_groups", c_int32), ("group_score", c_int32), ("renormalise", c_int32),
+                ("scale", ctypes.c_float), ("expert", c_void_p), ("weight", c_void_p), ("offsets", c_void_p),
+                ("src", c_void_p), ("dst", c_void_p), ("row_scale", c_void_p)]
+
+
+class _Block(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("terms", c_int32), ("post", c_int32), ("x_dtype", c_int32),
+                ("res_dtype", c_int32), ("post_dtype", c_int32), ("weight_dtype", c_int32), ("gate_dtype", c_int32),
+                ("y_dtype", c_int32), ("gate_act", c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("scale", ctypes.c_float), ("residual_scale", ctypes.c_float), ("x", c_void_p), ("ld_x", c_int64),
+                ("ld_term", c_int64), ("post_weight", c_void_p), ("gate", c_void_p), ("ld_gate", c_int64),
+                ("step_gate", c_int64), ("residual", c_void_p), ("ld_res", c_int64), ("weight", c_void_p),
+                ("total", c_void_p), ("ld_total", c_int64), ("y", c_void_p), ("ld_y", c_int64), ("y_scale", c_void_p)]
+
+
 _lib = None
 
 
@@ -162,6 +193,16 @@ def load():
     lib.fqm_gemm_grouped_workspace_size.argtypes = [P(_Weights), P(_Groups)]
     lib.fqm_gemm_grouped.restype = c_int32
     lib.fqm_gemm_grouped.argtypes = [P(_Weights), P(_Groups), c_void_p, ctypes.c_size_t, c_void_p]
+    lib.fqm_linear_workspace_size.restype = ctypes.c_size_t
+    lib.fqm_linear_workspace_size.argtypes = [P(_Weights), P(_Epilogue)]
+    lib.fqm_linear.restype = c_int32
+    lib.fqm_linear.argtypes = [P(_Weights), P(_Epilogue), c_void_p, ctypes.c_size_t, c_void_p]
+    lib.fqm_route_workspace_size.restype = ctypes.c_size_t
+    lib.fqm_route_workspace_size.argtypes = [P(_Routing)]
+    lib.fqm_route.restype = c_int32
+    lib.fqm_route.argtypes = [P(_Routing), c_void_p, ctypes.c_size_t, c_void_p]
+    lib.fqm_block_norm.restype = c_int32
+    lib.fqm_block_norm.argtypes = [P(_Block), c_void_p]
     _lib = lib
     return lib
 
@@ -580,3 +621,5 @@ def gemm(w: _WeightsBase, X: torch.Tensor, Y: torch.Tensor | None = None,
 
 from ._layer import (Adapters, NormOut, add_rms_norm, gemm_grouped,  # noqa: E402
                      gemm_grouped_workspace_size, lora, lora_workspace_size)
+from ._block import (Routing, block_norm, linear, linear_workspace_size, route,  # noqa: E402
+                     route_workspace_size)

@@ -553,6 +553,129 @@ bool groups_buffers_ok(const fqm_weights& w, const fqm_groups& g) {
            (!g.dst || in_allocation(g.dst, g.M * 4)) && (!g.row_scale || in_allocation(g.row_scale, g.M * 4));
 }
 
+// What the workspace depends on: sizes and types, no pointer of a.
+fqm_status check_linear_sizes(const fqm_weights* w, const fqm_epilogue* a) {
+    const fqm_status st = check_weights(w);
+    if (st != FQM_OK) return st;
+    if (!lut_format(*w)) return FQM_E_UNSUPPORTED;
+    if (!a) return FQM_E_NULL;
+    if (a->act < FQM_ACT_NONE || a->act > FQM_ACT_TANH || (a->gated != 0 && a->gated != 1) || !value_dtype(a->y_dtype))
+        return FQM_E_FORMAT;
+    if (a->M < 0 || a->M > kMaxRows || w->rows > kMaxRows || w->cols > (1 << 21) || (a->gated && w->rows % 2))
+        return FQM_E_SHAPE;
+    return FQM_OK;
+}
+
+fqm_status check_linear(const fqm_weights* w, const fqm_epilogue* a) {
+    const fqm_status st = check_linear_sizes(w, a);
+    if (st != FQM_OK || a->M == 0 || w->rows == 0) return st;
+    if ((a->bias && !value_dtype(a->bias_dtype)) || (a->residual && !value_dtype(a->res_dtype))) return FQM_E_FORMAT;
+    if (a->residual == a->Y && a->residual && (a->res_dtype != a->y_dtype || a->ld_res != a->ld_y)) return FQM_E_FORMAT;
+    if (!a->Y || (w->cols > 0 && !a->X)) return FQM_E_NULL;
+    const int64_t n = a->gated ? w->rows / 2 : w->rows;
+    if ((w->cols > 0 && (a->ld_x < w->cols || a->ld_x > (1 << 21))) || !rows_ok(a->M, a->ld_y, n) ||
+        (a->residual && !rows_ok(a->M, a->ld_res, n)))
+        return FQM_E_SHAPE;
+    if (!aligned16(a->X) || (w->cols > 0 && (a->ld_x & 7)) || !aligned_to(a->Y, dtype_bytes(a->y_dtype)) ||
+        (a->bias && !aligned_to(a->bias, dtype_bytes(a->bias_dtype))) ||
+        (a->residual && !aligned_to(a->residual, dtype_bytes(a->res_dtype))))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+bool linear_buffers_ok(const fqm_weights& w, const fqm_epilogue& a) {
+    const int64_t n = a.gated ? w.rows / 2 : w.rows;
+    return check_weight_buffers(w) == FQM_OK && (w.cols == 0 || in_allocation(a.X, span(a.M, a.ld_x, w.cols) * 2)) &&
+           (!a.bias || in_allocation(a.bias, w.rows * dtype_bytes(a.bias_dtype))) &&
+           (!a.residual || in_allocation(a.residual, span(a.M, a.ld_res, n) * dtype_bytes(a.res_dtype))) &&
+           in_allocation(a.Y, span(a.M, a.ld_y, n) * dtype_bytes(a.y_dtype));
+}
+
+// What the workspace depends on: sizes, no pointer of a but whether there is a plan.
+fqm_status check_route_sizes(const fqm_routing* a) {
+    if (!a) return FQM_E_NULL;
+    if (a->E < 1 || a->E > 1024 || a->k < 1 || a->k > 32 || a->groups < 1 || a->groups > 64 || a->top_groups < 1 ||
+        a->top_groups > a->groups)
+        return FQM_E_FORMAT;
+    if (a->E % a->groups || a->k > a->top_groups * (a->E / a->groups)) return FQM_E_SHAPE;
+    if (a->T < 0 || a->T > kMaxRows || a->T * a->k > kMaxRows) return FQM_E_SHAPE;
+    return FQM_OK;
+}
+
+fqm_status check_route(const fqm_routing* a) {
+    const fqm_status st = check_route_sizes(a);
+    if (st != FQM_OK) return st;
+    if (!value_dtype(a->x_dtype) || (a->score != FQM_SOFTMAX && a->score != FQM_SIGMOID) ||
+        (a->group_score != FQM_GROUP_MAX && a->group_score != FQM_GROUP_TOP2) ||
+        (a->renormalise != 0 && a->renormalise != 1) || !(a->scale >= -3.4e38f && a->scale <= 3.4e38f))
+        return FQM_E_FORMAT;
+    if (!aligned_to(a->offsets, 4)) return FQM_E_ALIGN;
+    if (a->T == 0) return FQM_OK;
+    if (!a->logits || !a->expert || !a->weight || (a->offsets && (!a->src || !a->dst || !a->row_scale))) return FQM_E_NULL;
+    if (!rows_ok(a->T, a->ld_x, a->E)) return FQM_E_SHAPE;
+    if (!aligned_to(a->logits, dtype_bytes(a->x_dtype)) || !aligned_to(a->bias, 4) || !aligned_to(a->expert, 4) ||
+        !aligned_to(a->weight, 4) ||
+        (a->offsets && (!aligned_to(a->src, 4) || !aligned_to(a->dst, 4) || !aligned_to(a->row_scale, 4))))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+bool route_buffers_ok(const fqm_routing& a) {
+    const int64_t slots = a.T * a.k * 4;
+    return in_allocation(a.logits, span(a.T, a.ld_x, a.E) * dtype_bytes(a.x_dtype)) &&
+           (!a.bias || in_allocation(a.bias, a.E * 4ll)) && in_allocation(a.expert, slots) && in_allocation(a.weight, slots) &&
+           (!a.offsets || (in_allocation(a.offsets, (a.E + 1) * 4ll) && in_allocation(a.src, slots) &&
+                           in_allocation(a.dst, slots) && in_allocation(a.row_scale, slots)));
+}
+
+fqm_status check_block(const fqm_block* a) {
+    if (!a) return FQM_E_NULL;
+    if (a->rows < 0 || a->rows > 0x7fffffff || a->cols < 0 || a->cols > 32768 || a->terms < 1 || a->terms > 64)
+        return FQM_E_SHAPE;
+    if (!value_dtype(a->x_dtype) || (a->residual && !value_dtype(a->res_dtype)) ||
+        (a->post_weight && !value_dtype(a->post_dtype)) || (a->weight && !value_dtype(a->weight_dtype)) ||
+        (a->gate && !value_dtype(a->gate_dtype)) || !(value_dtype(a->y_dtype) || a->y_dtype == FQM_I8) ||
+        a->gate_act < FQM_ACT_NONE || a->gate_act > FQM_ACT_TANH || (a->post != 0 && a->post != 1) ||
+        !(a->eps >= 0.f && a->eps <= 3.4e38f) || (a->gate && a->step_gate != 0 && a->step_gate != 1))
+        return FQM_E_FORMAT;
+    for (const float f : {a->weight_offset, a->scale, a->residual_scale})
+        if (!(f >= -3.4e38f && f <= 3.4e38f)) return FQM_E_FORMAT;
+    if (a->rows == 0) return FQM_OK;
+    const bool i8 = a->y_dtype == FQM_I8;
+    if (i8 && a->cols == 0 && !a->y_scale) return FQM_E_NULL;
+    if (i8 && !aligned_to(a->y_scale, 4)) return FQM_E_ALIGN;
+    if (a->cols == 0) return FQM_OK;
+    if (!a->x || (!a->y && !a->total) || (i8 && a->y && !a->y_scale)) return FQM_E_NULL;
+    if (!rows_ok(a->rows, a->ld_x, a->cols) || (a->terms > 1 && !rows_ok(a->terms, a->ld_term, a->cols)) ||
+        (a->residual && !rows_ok(a->rows, a->ld_res, a->cols)) ||
+        (a->gate && a->ld_gate != 0 && !rows_ok(a->rows, a->ld_gate, a->step_gate ? a->cols : 1)) ||
+        (a->total && !rows_ok(a->rows, a->ld_total, a->cols)) || (a->y && !rows_ok(a->rows, a->ld_y, a->cols)))
+        return FQM_E_SHAPE;
+    const int32_t total_dtype = a->residual ? a->res_dtype : a->x_dtype;
+    if (a->total && a->total == a->residual && a->ld_total != a->ld_res) return FQM_E_SHAPE;
+    if (!aligned_to(a->x, dtype_bytes(a->x_dtype)) || (a->y && !aligned_to(a->y, dtype_bytes(a->y_dtype))) ||
+        (a->residual && !aligned_to(a->residual, dtype_bytes(a->res_dtype))) ||
+        (a->post_weight && !aligned_to(a->post_weight, dtype_bytes(a->post_dtype))) ||
+        (a->weight && !aligned_to(a->weight, dtype_bytes(a->weight_dtype))) ||
+        (a->gate && !aligned_to(a->gate, dtype_bytes(a->gate_dtype))) ||
+        (a->total && !aligned_to(a->total, dtype_bytes(total_dtype))))
+        return FQM_E_ALIGN;
+    return FQM_OK;
+}
+
+bool block_buffers_ok(const fqm_block& a) {
+    const int64_t xb = dtype_bytes(a.x_dtype), rb = dtype_bytes(a.res_dtype);
+    const int64_t term = a.terms > 1 ? (a.terms - 1) * a.ld_term : 0;
+    return in_allocation(a.x, (span(a.rows, a.ld_x, a.cols) + term) * xb) &&
+           (!a.residual || in_allocation(a.residual, span(a.rows, a.ld_res, a.cols) * rb)) &&
+           (!a.post || !a.post_weight || in_allocation(a.post_weight, a.cols * dtype_bytes(a.post_dtype))) &&
+           (!a.y || !a.weight || in_allocation(a.weight, a.cols * dtype_bytes(a.weight_dtype))) &&
+           (!a.gate || in_allocation(a.gate, span(a.rows, a.ld_gate, a.step_gate ? a.cols : 1) * dtype_bytes(a.gate_dtype))) &&
+           (!a.total || in_allocation(a.total, span(a.rows, a.ld_total, a.cols) * (a.residual ? rb : xb))) &&
+           (!a.y || (in_allocation(a.y, span(a.rows, a.ld_y, a.cols) * dtype_bytes(a.y_dtype)) &&
+                     (a.y_dtype != FQM_I8 || in_allocation(a.y_scale, a.rows * 4))));
+}
+
 }  // namespace
 
 extern "C" {
@@ -621,6 +744,57 @@ fqm_status fqm_gemm_grouped(const fqm_weights* w, const fqm_groups* g, void* wor
     if (debug_on() && (!groups_buffers_ok(*w, *g) || (need && !in_allocation(workspace, (int64_t)need))))
         return FQM_E_BOUNDS;
     return debug_finish(hip_status(launch_grouped(*w, *g, workspace, s)), s);
+}
+
+size_t fqm_linear_workspace_size(const fqm_weights* w, const fqm_epilogue* a) {
+    if (check_linear_sizes(w, a) != FQM_OK || a->M == 0 || w->rows == 0) return 0;
+    return fqm::linear_workspace(*w, *a);
+}
+
+fqm_status fqm_linear(const fqm_weights* w, const fqm_epilogue* a, void* workspace, size_t ws_bytes, void* stream) {
+    const fqm_status st = check_linear(w, a);
+    if (st != FQM_OK || a->M == 0 || w->rows == 0) return st;
+    const size_t need = fqm::linear_workspace(*w, *a);
+    if (need && (!workspace || ws_bytes < need)) return FQM_E_WORKSPACE;
+    if (need && !aligned16(workspace)) return FQM_E_ALIGN;
+    hipStream_t s = as_stream(stream);
+    if (debug_on() && (!linear_buffers_ok(*w, *a) || (need && !in_allocation(workspace, (int64_t)need))))
+        return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_linear(*w, *a, workspace, s)), s);
+}
+
+size_t fqm_route_workspace_size(const fqm_routing* a) {
+    if (check_route_sizes(a) != FQM_OK || a->T == 0) return 0;
+    return fqm::route_workspace(*a);
+}
+
+fqm_status fqm_route(const fqm_routing* a, void* workspace, size_t ws_bytes, void* stream) {
+    const fqm_status st = check_route(a);
+    if (st != FQM_OK) return st;
+    hipStream_t s = as_stream(stream);
+    if (a->T == 0) {
+        if (!a->offsets) return FQM_OK;
+        if (debug_on() && !in_allocation(a->offsets, (a->E + 1) * 4ll)) return FQM_E_BOUNDS;
+        return debug_finish(hip_status(launch_zero_fill(a->offsets, a->E + 1, 4, s)), s);
+    }
+    const size_t need = fqm::route_workspace(*a);
+    if (need && (!workspace || ws_bytes < need)) return FQM_E_WORKSPACE;
+    if (need && !aligned16(workspace)) return FQM_E_ALIGN;
+    if (debug_on() && (!route_buffers_ok(*a) || (need && !in_allocation(workspace, (int64_t)need)))) return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_route(*a, workspace, s)), s);
+}
+
+fqm_status fqm_block_norm(const fqm_block* a, void* stream) {
+    const fqm_status st = check_block(a);
+    if (st != FQM_OK || a->rows == 0) return st;
+    hipStream_t s = as_stream(stream);
+    if (a->cols == 0) {
+        if (a->y_dtype != FQM_I8) return FQM_OK;
+        if (debug_on() && !in_allocation(a->y_scale, a->rows * 4)) return FQM_E_BOUNDS;
+        return debug_finish(hip_status(launch_zero_fill(a->y_scale, a->rows, 4, s)), s);
+    }
+    if (debug_on() && !block_buffers_ok(*a)) return FQM_E_BOUNDS;
+    return debug_finish(hip_status(launch_block_norm(*a, s)), s);
 }
 
 }  // extern "C"

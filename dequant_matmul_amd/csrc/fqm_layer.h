@@ -1,5 +1,6 @@
 // Internal declarations of the operators around the products: the residual
-// norm, the low-rank adapters and the products grouped by expert.
+// norm, the low-rank adapters, the products grouped by expert and their routing,
+// the product with an epilogue, the norms around a block.
 #pragma once
 
 #include "fqm_internal.h"
@@ -32,5 +33,13 @@ hipError_t launch_lora(const fqm_adapters& a, const uint16_t* x, const int32_t* 
 
 size_t grouped_workspace(const fqm_weights& w, const fqm_groups& g);
 hipError_t launch_grouped(const fqm_weights& w, const fqm_groups& g, void* ws, hipStream_t s);
+
+size_t linear_workspace(const fqm_weights& w, const fqm_epilogue& a);
+hipError_t launch_linear(const fqm_weights& w, const fqm_epilogue& a, void* ws, hipStream_t s);
+
+size_t route_workspace(const fqm_routing& a);
+hipError_t launch_route(const fqm_routing& a, void* ws, hipStream_t s);
+
+hipError_t launch_block_norm(const fqm_block& a, hipStream_t s);
 
 }  // namespace fqm

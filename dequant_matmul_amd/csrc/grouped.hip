@@ -377,7 +377,8 @@ __device__ __forceinline__ void grouped_tile(lds8* tab, lds8* x0, lds8* x1, lds8
         }
     };
     const int64_t w0 = (int64_t)e * a.N;
-    gemm_tile<BITS, BM, NW>(tab, x0, x1, x2, X, 0, x_off, a.packed + w0 * a.ld, a.ld, a.lut + (w0 << BITS), a.N, n0, t0,
+    gemm_tile<BITS, BM, NW>(tab, x0, x1, x2, X, 0, x_off, a.packed + w0 * a.ld, a.ld, a.lut + (w0 << BITS),
+                            RunOfRows{a.N, n0}, t0,
                             steps,
                             [&](int row, int col, float v) {
                                 const int n = n0 + col;

@@ -78,7 +78,7 @@ __device__ __forceinline__ void plan_tile(FQM_GEMM_ARGS) {
     const int t0 = (int)((int64_t)ks * ksteps / ksplit), t1 = (int)((int64_t)(ks + 1) * ksteps / ksplit);
     auto x_off = [&](int row) { return (uint32_t)(min(row, M - 1 - m0) * K) * 2u; };
     FQM_GEMM_TILE_LDS(BITS, BM, NWAVE);
-    gemm_tile<BITS, BM, NWAVE>(FQM_GEMM_TILE_LDS_ARGS, X, (uint32_t)m0 * (uint32_t)K * 2u, x_off, packed, ld, lut, N, n0, t0, t1 - t0,
+    gemm_tile<BITS, BM, NWAVE>(FQM_GEMM_TILE_LDS_ARGS, X, (uint32_t)m0 * (uint32_t)K * 2u, x_off, packed, ld, lut, RunOfRows{N, n0}, t0, t1 - t0,
                                [&](int row, int col, float v) {
                                    if constexpr (PARTIAL) {
                                        part[(size_t)b * (BM * BN) + row * BN + col] = v;

@@ -105,21 +105,30 @@ __device__ __forceinline__ void barrier_after_loads() {
     __shared__ __attribute__((aligned(16))) uint8_t s_x2[TileShape<BM, NW>::XT_BYTES]
 #define FQM_GEMM_TILE_LDS_ARGS (lds8*)s_tab, (lds8*)s_x0, (lds8*)s_x1, (lds8*)s_x2
 
-// The BM x 32 NW tile of W rows n0 .. n0 + 32 NW - 1 (rows past N - 1 repeat it)
-// over the K steps [t0, t0 + steps), steps >= 1.  x_off(row) is the byte offset
+// Rows n0 .. n0 + 32 NW - 1 of W as a tile's columns (rows past N - 1 repeat it).
+struct RunOfRows {
+    int N, n0;
+    __device__ __forceinline__ bool has(int r) const { return n0 + r < N; }
+    __device__ __forceinline__ int row(int r) const { return min(n0 + r, N - 1); }
+};
+
+// The tile of BM rows of X and the 32 NW rows of W that `wr` names: wr.row(r) is
+// tile column r's row of W, some row of it where there is none (wr.has(r)), over
+// the K steps [t0, t0 + steps), steps >= 1.  x_off(row) is the byte offset
 // of tile row `row` of X below X + xtile (32 bits in all; callers keep X below
 // 2 GiB from X on, and rows past the end at some valid row); out(row, col, v)
 // takes the fp32 sum of tile row `row` and tile column `col`, every one of
-// them, in a fixed order.  Where before is not NoPrep, before(scratch) runs ahead of
+// them, in a fixed order; an `out` of (block, sums) takes a wave's 32 x 32 blocks
+// of sums whole, as the matrix instruction leaves them.  Where before is not NoPrep, before(scratch) runs ahead of
 // the first out between two barriers, with at least 4 KB of LDS.
 // tab, x0, x1, x2: LDS objects of their own (FQM_GEMM_TILE_LDS), so that the
 // compiler sees that the table gathers do not wait for the direct loads of X.
 struct NoPrep {};
-template <int BITS, int BM, int NW, class XOff, class Out, class Prep = NoPrep>
+template <int BITS, int BM, int NW, class XOff, class WRows, class Out, class Prep = NoPrep>
 __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x2,
                                           const uint16_t* __restrict__ X, uint32_t xtile, XOff x_off,
                                           const uint8_t* __restrict__ packed, int64_t ld,
-                                          const uint16_t* __restrict__ lut, int N, int n0, int t0, int steps,
+                                          const uint16_t* __restrict__ lut, WRows wr, int t0, int steps,
                                           Out out, Prep before = Prep()) {
     using S = TileShape<BM, NW>;
     constexpr int MB = S::MB, XDMA = S::XDMA, BN = S::BN;
@@ -137,8 +146,8 @@ __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x
     for (int i = tid; i < BN * 8; i += 64 * NW) {
         const int r = i >> 3, part = i & 7;  // entries EPT part .. + EPT - 1 of tile row r
         uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (n0 + r < N) {
-            const uint16_t* src = lut + (int64_t)(n0 + r) * F::ENTRIES + part * EPT;
+        if (wr.has(r)) {
+            const uint16_t* src = lut + (int64_t)wr.row(r) * F::ENTRIES + part * EPT;
             if constexpr (EPT == 8) {
                 const u32x4 q = *reinterpret_cast<const u32x4*>(src);
                 v[0] = q[0]; v[1] = q[1]; v[2] = q[2]; v[3] = q[3];
@@ -179,7 +188,7 @@ __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x
     };
 
     // ---- codes: 24 bytes of row 32 wn + j per lane per step ------------------------
-    const uint8_t* csrc = packed + (int64_t)min(n0 + 32 * wn + j, N - 1) * ld + 4 * ND * g;
+    const uint8_t* csrc = packed + (int64_t)wr.row(32 * wn + j) * ld + 4 * ND * g;
     uint32_t cw[NXB][ND];
     auto load_codes = [&](int slot, int t) {
         const uint8_t* p = csrc + F::STEP_BYTES * t;
@@ -329,10 +338,15 @@ __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x
         __syncthreads();
     }
     // D layout of a 32x32 block: lane l, item r -> row (r % 4) + 8 * (r / 4) + 4 * (l / 32), column l % 32.
+    if constexpr (std::is_invocable<Out, int, const f32x16&>::value) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+        for (int i = 0; i < MB; ++i) out(i, acc[i]);
+    } else {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) out(32 * i + (r & 3) + 8 * (r >> 2) + 4 * g, 32 * wn + j, acc[i][r]);
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) out(32 * i + (r & 3) + 8 * (r >> 2) + 4 * g, 32 * wn + j, acc[i][r]);
+    }
 }
 
 }  // namespace

@@ -5,8 +5,10 @@
  * batch 1..16) and Y = X W^T (GEMM) where W is stored in one of three packed
  * formats and is decoded inside the kernels; W is never written out in full
  * (fqm_dequant exists for testing only).  Around them it has the residual norm
- * (fqm_add_rms_norm), low-rank adapters beside a product (fqm_lora) and
- * products grouped by expert (fqm_gemm_grouped).
+ * (fqm_add_rms_norm), low-rank adapters beside a product (fqm_lora),
+ * products grouped by expert (fqm_gemm_grouped) and the routing that groups
+ * them (fqm_route), the product with bias, activation and residual in its
+ * epilogue (fqm_linear) and the norms on both sides of a block (fqm_block_norm).
  *
  * Formats (pages named by title and section):
  *   FQM_LUT6  "Qwen3.8-27B - BenQ 6-bit", "What BenQ stores": one 6-bit code
@@ -105,8 +107,24 @@ typedef enum fqm_status {
 
 enum fqm_format { FQM_LUT6 = 1, FQM_FABQ = 2, FQM_MDBF = 3, FQM_LUT4 = 4 };
 /* FQM_I8 (two's complement, one fp32 scale per row) is an output of
- * fqm_add_rms_norm and an input of fqm_gemm_grouped only. */
+ * fqm_add_rms_norm and fqm_block_norm and an input of fqm_gemm_grouped only. */
 enum fqm_dtype { FQM_BF16 = 0, FQM_F32 = 1, FQM_I8 = 2 };
+/* Activations, in fp32:
+ *   RELU       max(v, 0)
+ *   SILU       v / (1 + exp(-v))
+ *   GELU       v * Phi(v), Phi the normal distribution's integral
+ *   GELU_TANH  v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
+ *   SIGMOID    1 / (1 + exp(-v))
+ *   TANH       tanh(v) */
+enum fqm_act {
+    FQM_ACT_NONE = 0,
+    FQM_ACT_RELU = 1,
+    FQM_ACT_SILU = 2,
+    FQM_ACT_GELU = 3,
+    FQM_ACT_GELU_TANH = 4,
+    FQM_ACT_SIGMOID = 5,
+    FQM_ACT_TANH = 6
+};
 
 /* Per-row LUT, 6-bit codes (rows = N outputs, cols = K inputs).
  * cols must be a multiple of 64 (one 48-byte group holds 64 codes). */
@@ -322,8 +340,9 @@ fqm_status fqm_gemm(const fqm_weights* w, const uint16_t* X, uint16_t* Y, int64_
 
 /* ---------------------------------------------------------------------------
  * What stands around the products in a decoder layer: the residual norm in
- * front of them, the adapters beside them, and the products of many experts.
- * Descriptors are HOST memory, read during the call only.  These three calls
+ * front of them, the adapters beside them, the products of many experts and
+ * their routing, the product with its epilogue, and the norms around a block.
+ * Descriptors are HOST memory, read during the call only.  These calls
  * handle NaN and infinities as the arithmetic below gives them; bf16 outputs
  * are rounded to nearest even.
  * ------------------------------------------------------------------------- */
@@ -441,6 +460,143 @@ size_t fqm_gemm_grouped_workspace_size(const fqm_weights* w, const fqm_groups* g
  * FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
 fqm_status fqm_gemm_grouped(const fqm_weights* w, const fqm_groups* g, void* workspace, size_t ws_bytes,
                             void* stream);
+
+/* What fqm_linear multiplies and does to the product.  Strides are in
+ * elements.  Rows of X start at multiples of 16 bytes (base aligned, ld_x a
+ * multiple of 8); residual and Y need only their element's alignment and any
+ * stride that holds a row. */
+typedef struct fqm_epilogue {
+    int64_t M;                  /* rows of X, 0..2^24 */
+    const uint16_t* X;          /* [M][ld_x] bf16, w->cols of each row are read */
+    int64_t ld_x;               /* w->cols <= ld_x <= 2^21 */
+    int32_t act;                /* enum fqm_act */
+    int32_t gated;              /* 0, or 1: W is two stacked matrices of n = w->rows / 2 rows */
+    const void* bias;           /* [w->rows], or NULL: zeros */
+    int32_t bias_dtype;         /* FQM_BF16 or FQM_F32 */
+    int32_t res_dtype;          /* FQM_BF16 or FQM_F32 */
+    const void* residual;       /* [M][ld_res], or NULL: zeros */
+    int64_t ld_res;
+    void* Y;                    /* [M][ld_y], n columns of each row (w->rows without gated) are written.
+                                   May be the residual itself (same dtype and stride). */
+    int64_t ld_y;
+    int32_t y_dtype;            /* FQM_BF16 or FQM_F32 */
+} fqm_epilogue;
+
+/* Bytes of device workspace fqm_linear needs on the current device (a function
+ * of w's rows, cols and format and of a's M, gated and types only; a's pointers
+ * may still be NULL); 0 for invalid arguments. */
+size_t fqm_linear_workspace_size(const fqm_weights* w, const fqm_epilogue* a);
+
+/* The product with everything that follows it up to the next operator:
+ *     v = W x + bias                                            (fp32)
+ *     y = residual + act(v)                                     (gated == 0)
+ *     y = residual + act(v[0 .. n-1]) * v[n .. 2n-1]            (gated == 1)
+ * for each row x of X, rounded once, to Y's type.  LUT6 or LUT4 weights, decoded
+ * inside the kernels as in fqm_gemv and fqm_gemm; w->cols a multiple of 64, at
+ * most 2^21; w->rows at most 2^24.  Any M: single tokens and prompts.  cols == 0
+ * counts as sums of nothing (v = bias).  workspace as for fqm_gemm.  Sums are
+ * added in a fixed order: results do not depend on timing, nor on the other
+ * rows' values.  FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
+fqm_status fqm_linear(const fqm_weights* w, const fqm_epilogue* a, void* workspace, size_t ws_bytes, void* stream);
+
+enum fqm_score { FQM_SOFTMAX = 0, FQM_SIGMOID = 1 };
+enum fqm_group_score {
+    FQM_GROUP_MAX = 0,  /* a group counts as its best expert */
+    FQM_GROUP_TOP2 = 1  /* as the sum of its two best scores (of one, where only one is open) */
+};
+
+/* Routing of T tokens to k of E experts each. */
+typedef struct fqm_routing {
+    int64_t T;                  /* tokens; T * k at most 2^24 */
+    int32_t E;                  /* 1..1024 */
+    int32_t k;                  /* 1..32, at most top_groups * E / groups */
+    const void* logits;         /* [T][ld_x], rows at their element's alignment */
+    int64_t ld_x;
+    int32_t x_dtype;            /* FQM_BF16 or FQM_F32 */
+    int32_t score;              /* enum fqm_score */
+    const float* bias;          /* [E], added to the scores for the choice alone, or NULL */
+    int32_t groups;             /* E falls into so many equal groups of neighbours, 1..64 */
+    int32_t top_groups;         /* groups that a token may choose from, 1..groups */
+    int32_t group_score;        /* enum fqm_group_score */
+    int32_t renormalise;        /* 1: a token's weights add up to `scale` */
+    float scale;                /* a factor of the weights, finite */
+    int32_t* expert;            /* [T][k] out: the chosen experts, best first; -1: none */
+    float* weight;              /* [T][k] out */
+    int32_t* offsets;           /* [E + 1] out, or NULL: no plan (then the next three are not used) */
+    int32_t* src;               /* [T * k] out */
+    int32_t* dst;               /* [T * k] out */
+    float* row_scale;           /* [T * k] out */
+} fqm_routing;
+
+/* Bytes of device workspace fqm_route needs (a function of T, E, k and of
+ * whether offsets is there); 0 for invalid arguments. */
+size_t fqm_route_workspace_size(const fqm_routing* a);
+
+/* Each token's experts, their weights, and the plan of their products.
+ *   score    s = softmax(logits) over the open experts, or 1 / (1 + exp(-logits))
+ *   choice   c = s + bias; without a bias the order is that of the logits
+ *   groups   the top_groups groups of best group score stay (ties: the lowest group)
+ *   experts  the k of them with the largest c, best first (ties: the lowest index)
+ *   weight   scale * s, with renormalise scale * s / (sum of the chosen s)
+ * The choice is that of exact scores (scores too near each other for fp32 are
+ * formed again in fp64).  An expert is closed to a token whose logit for it is
+ * -infinity or NaN (so is one whose bias is): it is never chosen, has no part
+ * in the softmax, and a group without an open expert comes last.  A logit of
+ * +infinity counts as fp32's largest number.  A token with fewer than k open
+ * experts in its groups has expert -1 and weight 0 in the places that are left.
+ * The plan lists the T * k slots (slot t k + j: token t's j-th expert) by expert,
+ * a slot's number deciding within one expert, as fqm_gemm_grouped takes them:
+ * offsets[e] .. offsets[e+1]-1 are expert e's rows, src their tokens, dst their
+ * slots, row_scale their weights.  Slots without an expert stand behind the
+ * others, as rows of the last expert with src -1 and row_scale 0: the product
+ * by src and dst stores zeros for them.
+ * Results do not depend on timing.  T == 0 writes zeros to offsets. */
+fqm_status fqm_route(const fqm_routing* a, void* workspace, size_t ws_bytes, void* stream);
+
+/* Rows of fqm_block_norm.  Strides are in elements; rows need only their
+ * element's alignment and any stride that holds a row. */
+typedef struct fqm_block {
+    int64_t rows, cols;         /* cols 0..32768 */
+    int32_t terms;              /* 1..64 vectors of x added per row */
+    int32_t post;               /* 1: the sum is normed before the gate, 0: it is not */
+    int32_t x_dtype;            /* FQM_BF16 or FQM_F32, as the next four */
+    int32_t res_dtype;
+    int32_t post_dtype;
+    int32_t weight_dtype;
+    int32_t gate_dtype;
+    int32_t y_dtype;            /* FQM_BF16, FQM_F32 or FQM_I8 */
+    int32_t gate_act;           /* enum fqm_act, applied to the gate */
+    float eps;                  /* of both norms, >= 0 */
+    float weight_offset;        /* added to both norms' weights (1 where they are stored less one) */
+    float scale;                /* of the block's output */
+    float residual_scale;       /* of the residual */
+    const void* x;              /* element (row, term, col) at row*ld_x + term*ld_term + col */
+    int64_t ld_x, ld_term;      /* ld_term is not read with one term */
+    const void* post_weight;    /* [cols], or NULL: the norm's factor is 1 */
+    const void* gate;           /* element (row, col) at row*ld_gate + col*step_gate, or NULL: 1 */
+    int64_t ld_gate, step_gate; /* ld_gate 0: one row for all; step_gate 1, or 0: one value per row */
+    const void* residual;       /* [rows][ld_res], or NULL: zeros */
+    int64_t ld_res;
+    const void* weight;         /* [cols], or NULL: the norm's factor is 1 */
+    void* total;                /* [rows][ld_total], or NULL: not stored; its dtype is the residual's, or x's
+                                   without one.  May be the residual itself. */
+    int64_t ld_total;
+    void* y;                    /* [rows][ld_y], or NULL: no second norm */
+    int64_t ld_y;
+    float* y_scale;             /* [rows], required for FQM_I8, not used otherwise */
+} fqm_block;
+
+/* The norm behind a block, its gate and scales, the residual's addition, and
+ * the norm in front of the next block, in one pass:
+ *     u = sum over terms of x                                              (fp32)
+ *     v = u * (post_weight + weight_offset) / sqrt(mean(u^2) + eps)        (post; v = u otherwise)
+ *     h = residual_scale * residual + scale * gate_act(gate) * v
+ *     y = h * (weight + weight_offset) / sqrt(mean(h^2) + eps)
+ * total receives h rounded to its dtype (y is formed from the unrounded h), y
+ * and y_scale as in fqm_add_rms_norm.  The means are fp32: where u or h passes
+ * about 2^63 they are infinite and the norm zeros.  rows == 0 enqueues nothing;
+ * cols == 0 writes zeros to y_scale. */
+fqm_status fqm_block_norm(const fqm_block* a, void* stream);
 
 #ifdef __cplusplus
 }

@@ -23,9 +23,11 @@ library matrix product:
           "Algorithm" and "Bit-width and rank").
   layer - the operators around the products (residual norm, low-rank
           adapters, products grouped by expert) with bounds on fp32's error.
+  block - what completes a block (the product with its epilogue, the routing to
+          experts, the norms on both sides of a block), with such bounds.
 
 Pins that tie each part to something other than itself live in
 ``tests/test_oracle_*.py``.  Parity status per function is stated in each
 module header.
 """
-from . import numerics, bits, lut6, lut4, fabq, mdbf, compare, layer  # noqa: F401
+from . import numerics, bits, lut6, lut4, fabq, mdbf, compare, layer, block  # noqa: F401
