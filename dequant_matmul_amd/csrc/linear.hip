@@ -34,20 +34,102 @@ struct StackedRows {
     __device__ __forceinline__ int row(int r) const { return min(output(r), n - 1) + (r >> 4 & 1) * n; }
 };
 
+// 4 values at their element's alignment (gfx950's global accesses take any).
+typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_e __attribute__((aligned(4)));
+
 __device__ __forceinline__ float load_value(const void* p, int dtype, int64_t at) {
     return dtype == FQM_F32 ? static_cast<const float*>(p)[at] : bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
 }
-__device__ __forceinline__ void store_value(void* p, int dtype, int64_t at, float v) {
-    if (dtype == FQM_F32) static_cast<float*>(p)[at] = v;
-    else static_cast<uint16_t*>(p)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+__device__ __forceinline__ f32x4 load_4(const void* p, int dtype, int64_t at, int n) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (n == 4) {
+        if (dtype == FQM_F32) return *reinterpret_cast<const f32x4_e*>(static_cast<const float*>(p) + at);
+        const u32x2_e q = *reinterpret_cast<const u32x2_e*>(static_cast<const uint16_t*>(p) + at);
+        return f32x4{bf16lo(q[0]), bf16hi(q[0]), bf16lo(q[1]), bf16hi(q[1])};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] = load_value(p, dtype, at + i);
+    return v;
 }
-__device__ __forceinline__ float bias_of(const fqm_epilogue& a, int row) {
-    return a.bias ? load_value(a.bias, a.bias_dtype, row) : 0.f;
+__device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ __forceinline__ void store_4(void* p, int dtype, int64_t at, f32x4 v, int n) {
+    if (dtype == FQM_F32) {
+        float* q = static_cast<float*>(p) + at;
+        if (n == 4) {
+            *reinterpret_cast<f32x4_e*>(q) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) q[i] = v[i];
+        }
+    } else {
+        uint16_t* q = static_cast<uint16_t*>(p) + at;
+        if (n == 4) {
+            *reinterpret_cast<u32x2_e*>(q) = u32x2_e{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) q[i] = (uint16_t)bf16_bits(v[i]);
+        }
+    }
 }
-// u of row m and column c to its place
-__device__ __forceinline__ void finish(const fqm_epilogue& a, int64_t m, int c, float u) {
-    if (a.residual) u += load_value(a.residual, a.res_dtype, m * a.ld_res + c);
-    store_value(a.Y, a.y_dtype, m * a.ld_y + c, u);
+__device__ __forceinline__ f32x4 bias_4(const fqm_epilogue& a, int row, int n) {
+    return a.bias ? load_4(a.bias, a.bias_dtype, row, n) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Outputs c .. c + 3 of row m (n of them) from their sums v, and w of the second matrix.
+template <bool GATED>
+__device__ __forceinline__ void finish(const Linear& p, int64_t m, int c, f32x4 v, f32x4 w, int n) {
+    const fqm_epilogue& a = p.a;
+    if (n <= 0) return;
+    const f32x4 b = bias_4(a, c, n);
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (a.residual) r = load_4(a.residual, a.res_dtype, m * a.ld_res + c, n);
+    f32x4 wb = {0.f, 0.f, 0.f, 0.f};
+    if (GATED) wb = bias_4(a, p.n + c, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = activate(a.act, v[i] + b[i]);
+        if (GATED) v[i] *= w[i] + wb[i];
+        if (a.residual) v[i] += r[i];
+    }
+    store_4(a.Y, a.y_dtype, m * a.ld_y + c, v, n);
+}
+
+typedef __attribute__((address_space(3))) float lds_f;
+typedef __attribute__((address_space(3))) f32x4 lds_f4;
+
+// A wave's 32 x 32 block of sums, as the matrix instruction leaves it (lane l, item r: row
+// (r % 4) + 8 (r / 4) + 4 (l / 32), column l % 32), through 1 KB of LDS of its own to rows of 4
+// columns a lane: 8 rows at a time, items 4 q .. 4 q + 3.  m, c: Y's row and column of the block's
+// first; rows: how many of its rows there are.
+template <bool GATED>
+__device__ __forceinline__ void finish_block(const Linear& p, lds8* own, const f32x16& acc, int64_t m, int c, int rows) {
+    const int lane = threadIdx.x & 63, j = lane & 31, g = lane >> 5;
+    lds_f* put = (lds_f*)own + 128 * g + j;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) put[32 * r] = acc[4 * q + r];
+        wave_lds_order();
+        if constexpr (GATED) {
+            const int row = lane >> 2, o = 4 * (lane & 3);  // lanes 0..31: 8 rows of 16 outputs
+            if (lane < 32 && 8 * q + row < rows) {
+                const f32x4 v = *(lds_f4*)((lds_f*)own + 32 * row + o), w = *(lds_f4*)((lds_f*)own + 32 * row + 16 + o);
+                finish<true>(p, m + 8 * q + row, c + o, v, w, min(4, p.n - c - o));
+            }
+        } else {
+            const int row = lane >> 3, o = 4 * (lane & 7);
+            if (8 * q + row < rows) {
+                const f32x4 v = *(lds_f4*)((lds_f*)own + 32 * row + o);
+                finish<false>(p, m + 8 * q + row, c + o, v, v, min(4, p.n - c - o));
+            }
+        }
+        wave_lds_order();
+    }
 }
 
 // Workgroup b: M tile tt % mtiles and N tile nt0 + tt / mtiles, tt = b / ksplit, over the
@@ -55,7 +137,7 @@ __device__ __forceinline__ void finish(const fqm_epilogue& a, int64_t m, int c, 
 template <int BITS, int BM, int NW, bool GATED, bool PARTIAL>
 __global__ __launch_bounds__(64 * NW) void linear_tile_kernel(const Linear p, int mtiles, int nt0, int ksplit,
                                                               float* __restrict__ part) {
-    constexpr int BN = 32 * NW;
+    constexpr int BN = 32 * NW, OUT = GATED ? BN / 2 : BN;
     FQM_GEMM_TILE_LDS(BITS, BM, NW);
     const fqm_epilogue& a = p.a;
     const int b = blockIdx.x, tt = b / ksplit, ks = b - tt * ksplit;
@@ -64,113 +146,123 @@ __global__ __launch_bounds__(64 * NW) void linear_tile_kernel(const Linear p, in
     const int rows = (int)min((int64_t)BM, a.M - m0), ksteps = p.K / BK;
     const int t0 = (int)((int64_t)ks * ksteps / ksplit), t1 = (int)((int64_t)(ks + 1) * ksteps / ksplit);
     auto x_off = [&](int row) { return (uint32_t)min(row, rows - 1) * (uint32_t)a.ld_x * 2u; };
-    const uint16_t* X = a.X + m0 * a.ld_x;
-    auto tile = [&](auto wr, auto out) {
-        gemm_tile<BITS, BM, NW>(FQM_GEMM_TILE_LDS_ARGS, X, 0, x_off, p.packed, p.ld, p.lut, wr, t0, t1 - t0, out);
+    auto tile = [&](auto wr) {
+        const uint16_t* X = a.X + m0 * a.ld_x;
+        if constexpr (PARTIAL)
+            gemm_tile<BITS, BM, NW>(FQM_GEMM_TILE_LDS_ARGS, X, 0, x_off, p.packed, p.ld, p.lut, wr, t0, t1 - t0,
+                                    [&](int row, int col, float v) { part[(size_t)b * (BM * BN) + row * BN + col] = v; });
+        else
+            gemm_tile<BITS, BM, NW>(FQM_GEMM_TILE_LDS_ARGS, X, 0, x_off, p.packed, p.ld, p.lut, wr, t0, t1 - t0,
+                                    [&](int i, const f32x16& acc) {
+                                        const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                        finish_block<GATED>(p, (lds8*)s_x0 + 1024 * wn, acc, m0 + 32 * i, nt * OUT + OUT / NW * wn,
+                                                            rows - 32 * i);
+                                    });
     };
-    const int lane = threadIdx.x & 63, j = lane & 31, g = lane >> 5, wn = threadIdx.x >> 6;
-    auto row_of = [&](int i, int r) { return 32 * i + (r & 3) + 8 * (r >> 2) + 4 * g; };
-    if constexpr (PARTIAL) {
-        auto out = [&](int row, int col, float v) { part[(size_t)b * (BM * BN) + row * BN + col] = v; };
-        if constexpr (GATED) tile(StackedRows{p.n, nt * (BN / 2)}, out);
-        else tile(RunOfRows{p.N, nt * BN}, out);
-    } else if constexpr (GATED) {
-        const StackedRows wr{p.n, nt * (BN / 2)};
-        const int c = wr.output(32 * wn + j);
-        const float bias = bias_of(a, wr.row(32 * wn + j));
-        tile(wr, [&](int i, const f32x16& acc) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float v = acc[r] + bias, o = __shfl_xor(v, 16, 64);
-                const int row = row_of(i, r);
-                if (j < 16 && row < rows && c < p.n) finish(a, m0 + row, c, activate(a.act, v) * o);
-            }
-        });
-    } else {
-        const RunOfRows wr{p.N, nt * BN};
-        const int c = wr.n0 + 32 * wn + j;
-        const float bias = bias_of(a, wr.row(32 * wn + j));
-        tile(wr, [&](int i, const f32x16& acc) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = row_of(i, r);
-                if (row < rows && c < p.n) finish(a, m0 + row, c, activate(a.act, acc[r] + bias));
-            }
-        });
-    }
+    if constexpr (GATED) tile(StackedRows{p.n, nt * OUT});
+    else tile(RunOfRows{p.N, nt * OUT});
 }
 
-// Y of the split tiles: the parts' sums in order, then the epilogue.  One output a thread.
+// Y of the split tiles: the parts' sums in order, then the epilogue.  4 outputs a thread.
 template <int BM, int NW, bool GATED>
 __global__ __launch_bounds__(256) void linear_reduce(const Linear p, const float* __restrict__ part, int mtiles, int nt0,
-                                                     int ksplit, int64_t outputs) {
+                                                     int ksplit, int64_t groups) {
     constexpr int BN = 32 * NW, OUT = GATED ? BN / 2 : BN;
-    const fqm_epilogue& a = p.a;
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= outputs) return;
-    const int64_t tt = e / (BM * OUT);
-    const int rem = (int)(e - tt * (BM * OUT)), row = rem / OUT, o = rem - row * OUT;
+    if (e >= groups) return;
+    const int64_t tt = e / (BM * OUT / 4);
+    const int rem = (int)(e - tt * (BM * OUT / 4)), row = rem / (OUT / 4), o = 4 * (rem - row * (OUT / 4));
     const int64_t m = (tt % mtiles) * BM + row;
     const int c = (int)(nt0 + tt / mtiles) * OUT + o;
-    if (m >= a.M || c >= p.n) return;
-    const int col = GATED ? 32 * (o >> 4) + (o & 15) : o;
-    const float* q = part + (size_t)tt * ksplit * (BM * BN) + row * BN + col;
-    float v = 0.f, w = 0.f;
-    for (int k = 0; k < ksplit; ++k) {
-        v += q[(size_t)k * (BM * BN)];
-        if (GATED) w += q[(size_t)k * (BM * BN) + 16];
+    if (m >= p.a.M || c >= p.n) return;
+    const float* q = part + (size_t)tt * ksplit * (BM * BN) + row * BN + (GATED ? 32 * (o >> 4) + (o & 15) : o);
+    f32x4 v = *reinterpret_cast<const f32x4*>(q), w = v;
+    if (GATED) w = *reinterpret_cast<const f32x4*>(q + 16);
+    for (int k = 1; k < ksplit; ++k) {
+        v += *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN));
+        if (GATED) w += *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN) + 16);
     }
-    float u = activate(a.act, v + bias_of(a, c));
-    if (GATED) u *= w + bias_of(a, p.n + c);
-    finish(a, m, c, u);
+    finish<GATED>(p, m, c, v, w, min(4, p.n - c));
 }
 
 // cols == 0: the sums are of nothing.
 __global__ __launch_bounds__(256) void linear_of_nothing(const Linear p, int64_t outputs) {
-    const fqm_epilogue& a = p.a;
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e >= outputs) return;
     const int64_t m = e / p.n;
     const int c = (int)(e - m * p.n);
-    float u = activate(a.act, bias_of(a, c));
-    if (a.gated) u *= bias_of(a, p.n + c);
-    finish(a, m, c, u);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    if (p.a.gated) finish<true>(p, m, c, zero, zero, 1);
+    else finish<false>(p, m, c, zero, zero, 1);
 }
 
+// Tiles and what is split.  Up to 256 rows all tiles are split alike, so that the
+// grid has enough workgroups; above, whole rounds of 256-row tiles (one per compute
+// unit) run as one launch and the N tiles that are left for a partial round are split
+// along K into as many parts as make that round shortest.
 struct LinearPlan {
-    int bm, nw, mtiles, ntiles, ksplit;
+    int bm, nw, mtiles, ntiles;
+    int nt_main;      // N tiles [0, nt_main) are not split
+    int ksplit;       // K parts of the others
+    int64_t tail;     // the others
     size_t part_bytes;
 };
+
+// Of the current device (without one, an MI355X's).
+int compute_units() {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    return std::max(cus, 1);
+}
 
 LinearPlan linear_plan(int64_t N, int64_t K, int64_t M, bool gated) {
     LinearPlan p;
     p.bm = M <= 32 ? 32 : M <= 256 ? 64 : 256;
     p.nw = p.bm == 256 ? 8 : 4;
-    const int64_t per = gated ? 16 * p.nw : 32 * p.nw, n = gated ? N / 2 : N;
+    const int64_t per = gated ? 16 * p.nw : 32 * p.nw, n = gated ? N / 2 : N, steps = K / BK;
     p.mtiles = (int)((M + p.bm - 1) / p.bm);
-    p.ntiles = (int)((n + per - 1) / per);
-    const int64_t tiles = (int64_t)p.mtiles * p.ntiles, want = p.bm == 256 ? 256 : 768;
-    p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>({want / std::max<int64_t>(tiles, 1), K / BK / 8, (int64_t)8}));
-    p.part_bytes = p.ksplit > 1 ? (size_t)tiles * p.ksplit * p.bm * 32 * p.nw * 4 : 0;
+    p.ntiles = p.nt_main = (int)((n + per - 1) / per);
+    p.ksplit = 1;
+    p.tail = 0;
+    const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+    if (p.bm < 256) {
+        const int64_t parts = std::min<int64_t>({768 / tiles, steps / 8, (int64_t)8});
+        if (parts > 1) p.ksplit = (int)parts, p.nt_main = 0;
+    } else if (const int64_t slots = compute_units(); tiles % slots) {
+        const int nt_main = (int)(tiles / slots * slots / p.mtiles);
+        const int64_t tail = (int64_t)(p.ntiles - nt_main) * p.mtiles;
+        int64_t best = (tail + slots - 1) / slots * steps;
+        for (int64_t k = 2; k <= steps / 8 && tail * k * (256 * 256 * 4) <= ((int64_t)256 << 20); ++k) {
+            const int64_t len = (tail * k + slots - 1) / slots * ((steps + k - 1) / k);
+            if (len < best) best = len, p.ksplit = (int)k, p.nt_main = nt_main;
+        }
+    }
+    p.tail = (int64_t)(p.ntiles - p.nt_main) * p.mtiles;
+    p.part_bytes = (size_t)p.tail * p.ksplit * p.bm * 32 * p.nw * 4;
     return p;
 }
 
 template <int BITS, int BM, int NW, bool GATED>
 hipError_t launch_tiles(const Linear& p, const LinearPlan& plan, float* part, hipStream_t s) {
-    const int64_t tiles = (int64_t)plan.mtiles * plan.ntiles, grid = tiles * plan.ksplit;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    if (plan.ksplit == 1) {
-        hipLaunchKernelGGL((linear_tile_kernel<BITS, BM, NW, GATED, false>), dim3((unsigned)grid), dim3(64 * NW), 0, s, p,
+    const int64_t main_tiles = (int64_t)plan.nt_main * plan.mtiles, grid = plan.tail * plan.ksplit;
+    if (main_tiles > 0x7fffffff || grid > 0x7fffffff) return hipErrorInvalidValue;
+    hipError_t e = hipSuccess;
+    if (main_tiles > 0) {
+        hipLaunchKernelGGL((linear_tile_kernel<BITS, BM, NW, GATED, false>), dim3((unsigned)main_tiles), dim3(64 * NW), 0, s, p,
                            plan.mtiles, 0, 1, nullptr);
-        return hipGetLastError();
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
+    if (plan.tail == 0) return e;
     hipLaunchKernelGGL((linear_tile_kernel<BITS, BM, NW, GATED, true>), dim3((unsigned)grid), dim3(64 * NW), 0, s, p,
-                       plan.mtiles, 0, plan.ksplit, part);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t outputs = tiles * BM * (GATED ? 16 * NW : 32 * NW);
-    hipLaunchKernelGGL((linear_reduce<BM, NW, GATED>), dim3((unsigned)((outputs + 255) / 256)), dim3(256), 0, s, p, part,
-                       plan.mtiles, 0, plan.ksplit, outputs);
+                       plan.mtiles, plan.nt_main, plan.ksplit, part);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t groups = plan.tail * BM * (GATED ? 4 * NW : 8 * NW);
+    if ((groups + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((linear_reduce<BM, NW, GATED>), dim3((unsigned)((groups + 255) / 256)), dim3(256), 0, s, p, part,
+                       plan.mtiles, plan.nt_main, plan.ksplit, groups);
     return hipGetLastError();
 }
 

@@ -119,7 +119,8 @@ struct RunOfRows {
 // 2 GiB from X on, and rows past the end at some valid row); out(row, col, v)
 // takes the fp32 sum of tile row `row` and tile column `col`, every one of
 // them, in a fixed order; an `out` of (block, sums) takes a wave's 32 x 32 blocks
-// of sums whole, as the matrix instruction leaves them.  Where before is not NoPrep, before(scratch) runs ahead of
+// of sums whole, as the matrix instruction leaves them, behind a barrier after which
+// no wave touches the LDS any more.  Where before is not NoPrep, before(scratch) runs ahead of
 // the first out between two barriers, with at least 4 KB of LDS.
 // tab, x0, x1, x2: LDS objects of their own (FQM_GEMM_TILE_LDS), so that the
 // compiler sees that the table gathers do not wait for the direct loads of X.
@@ -339,8 +340,16 @@ __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x
     }
     // D layout of a 32x32 block: lane l, item r -> row (r % 4) + 8 * (r / 4) + 4 * (l / 32), column l % 32.
     if constexpr (std::is_invocable<Out, int, const f32x16&>::value) {
+        __syncthreads();
+        // one copy of `out`, whose code may be long: eight of them left the sums in scratch memory
+#pragma unroll 1
+        for (int i = 0; i < MB; ++i) {
+            f32x16 sums = acc[0];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) out(i, acc[i]);
+            for (int b = 1; b < MB; ++b)
+                if (i == b) sums = acc[b];
+            out(i, sums);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < MB; ++i)
