@@ -34,101 +34,101 @@ struct StackedRows {
     __device__ __forceinline__ int row(int r) const { return min(output(r), n - 1) + (r >> 4 & 1) * n; }
 };
 
-// 4 values at their element's alignment (gfx950's global accesses take any).
-typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef f32x4 f32x4_e __attribute__((aligned(4)));
+// V values (2 or 4) at their element's alignment (gfx950's global accesses take any).
+template <int V>
+struct Values {
+    typedef float f32 __attribute__((ext_vector_type(V)));
+    typedef f32 f32_at __attribute__((aligned(4)));
+    typedef uint16_t u16 __attribute__((ext_vector_type(V)));
+    typedef u16 u16_at __attribute__((aligned(2)));
+};
 
 __device__ __forceinline__ float load_value(const void* p, int dtype, int64_t at) {
     return dtype == FQM_F32 ? static_cast<const float*>(p)[at] : bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
 }
-__device__ __forceinline__ f32x4 load_4(const void* p, int dtype, int64_t at, int n) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (n == 4) {
-        if (dtype == FQM_F32) return *reinterpret_cast<const f32x4_e*>(static_cast<const float*>(p) + at);
-        const u32x2_e q = *reinterpret_cast<const u32x2_e*>(static_cast<const uint16_t*>(p) + at);
-        return f32x4{bf16lo(q[0]), bf16hi(q[0]), bf16lo(q[1]), bf16hi(q[1])};
-    }
+// n of them, the others 0
+template <int V>
+__device__ __forceinline__ void load_values(const void* p, int dtype, int64_t at, int n, float (&v)[V]) {
+    if (n == V && dtype == FQM_F32) {
+        const auto q = *reinterpret_cast<const typename Values<V>::f32_at*>(static_cast<const float*>(p) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) v[i] = load_value(p, dtype, at + i);
-    return v;
-}
-__device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
-__device__ __forceinline__ void store_4(void* p, int dtype, int64_t at, f32x4 v, int n) {
-    if (dtype == FQM_F32) {
-        float* q = static_cast<float*>(p) + at;
-        if (n == 4) {
-            *reinterpret_cast<f32x4_e*>(q) = v;
-        } else {
+        for (int i = 0; i < V; ++i) v[i] = q[i];
+    } else if (n == V) {
+        const auto q = *reinterpret_cast<const typename Values<V>::u16_at*>(static_cast<const uint16_t*>(p) + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) q[i] = v[i];
-        }
+        for (int i = 0; i < V; ++i) v[i] = bf16_to_f32(q[i]);
     } else {
-        uint16_t* q = static_cast<uint16_t*>(p) + at;
-        if (n == 4) {
-            *reinterpret_cast<u32x2_e*>(q) = u32x2_e{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
-        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) q[i] = (uint16_t)bf16_bits(v[i]);
-        }
+        for (int i = 0; i < V; ++i) v[i] = i < n ? load_value(p, dtype, at + i) : 0.f;
     }
 }
-__device__ __forceinline__ f32x4 bias_4(const fqm_epilogue& a, int row, int n) {
-    return a.bias ? load_4(a.bias, a.bias_dtype, row, n) : f32x4{0.f, 0.f, 0.f, 0.f};
+template <int V>
+__device__ __forceinline__ void store_values(void* p, int dtype, int64_t at, const float (&v)[V], int n) {
+    typename Values<V>::u16 h;
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+    float* pf = static_cast<float*>(p) + at;
+    uint16_t* ph = static_cast<uint16_t*>(p) + at;
+    if (n == V && dtype == FQM_F32) {
+        typename Values<V>::f32 q;
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = v[i];
+        *reinterpret_cast<typename Values<V>::f32_at*>(pf) = q;
+    } else if (n == V) {
+        *reinterpret_cast<typename Values<V>::u16_at*>(ph) = h;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) {
+                if (dtype == FQM_F32) pf[i] = v[i];
+                else ph[i] = h[i];
+            }
+    }
 }
 
-// Outputs c .. c + 3 of row m (n of them) from their sums v, and w of the second matrix.
-template <bool GATED>
-__device__ __forceinline__ void finish(const Linear& p, int64_t m, int c, f32x4 v, f32x4 w, int n) {
+// Outputs c .. c + V - 1 of row m (n of them) from their sums v, and w of the second matrix.
+template <bool GATED, int V>
+__device__ __forceinline__ void finish(const Linear& p, int64_t m, int c, float (&v)[V], const float (&w)[V], int n) {
     const fqm_epilogue& a = p.a;
     if (n <= 0) return;
-    const f32x4 b = bias_4(a, c, n);
-    f32x4 r = {0.f, 0.f, 0.f, 0.f};
-    if (a.residual) r = load_4(a.residual, a.res_dtype, m * a.ld_res + c, n);
-    f32x4 wb = {0.f, 0.f, 0.f, 0.f};
-    if (GATED) wb = bias_4(a, p.n + c, n);
+    float b[V], wb[V], r[V];
+    if (a.residual) load_values<V>(a.residual, a.res_dtype, m * a.ld_res + c, n, r);
+    if (a.bias) {
+        load_values<V>(a.bias, a.bias_dtype, c, n, b);
+        if (GATED) load_values<V>(a.bias, a.bias_dtype, p.n + c, n, wb);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = activate(a.act, v[i] + b[i]);
-        if (GATED) v[i] *= w[i] + wb[i];
+    for (int i = 0; i < V; ++i) {
+        v[i] = activate(a.act, a.bias ? v[i] + b[i] : v[i]);
+        if (GATED) v[i] *= a.bias ? w[i] + wb[i] : w[i];
         if (a.residual) v[i] += r[i];
     }
-    store_4(a.Y, a.y_dtype, m * a.ld_y + c, v, n);
+    store_values<V>(a.Y, a.y_dtype, m * a.ld_y + c, v, n);
 }
 
 typedef __attribute__((address_space(3))) float lds_f;
-typedef __attribute__((address_space(3))) f32x4 lds_f4;
 
 // A wave's 32 x 32 block of sums, as the matrix instruction leaves it (lane l, item r: row
-// (r % 4) + 8 (r / 4) + 4 (l / 32), column l % 32), through 1 KB of LDS of its own to rows of 4
-// columns a lane: 8 rows at a time, items 4 q .. 4 q + 3.  m, c: Y's row and column of the block's
+// (r % 4) + 8 (r / 4) + 4 (l / 32), column l % 32), through 1 KB of LDS of its own to neighbouring
+// outputs on a lane: 8 rows at a time, items 4 q .. 4 q + 3.  m, c: Y's row and column of the block's
 // first; rows: how many of its rows there are.
 template <bool GATED>
 __device__ __forceinline__ void finish_block(const Linear& p, lds8* own, const f32x16& acc, int64_t m, int c, int rows) {
+    constexpr int V = GATED ? 2 : 4;  // outputs of a lane
     const int lane = threadIdx.x & 63, j = lane & 31, g = lane >> 5;
     lds_f* put = (lds_f*)own + 128 * g + j;
+    const int row = lane >> 3, o = V * (lane & 7);
+    const lds_f* get = (lds_f*)own + 32 * row + o;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) put[32 * r] = acc[4 * q + r];
         wave_lds_order();
-        if constexpr (GATED) {
-            const int row = lane >> 2, o = 4 * (lane & 3);  // lanes 0..31: 8 rows of 16 outputs
-            if (lane < 32 && 8 * q + row < rows) {
-                const f32x4 v = *(lds_f4*)((lds_f*)own + 32 * row + o), w = *(lds_f4*)((lds_f*)own + 32 * row + 16 + o);
-                finish<true>(p, m + 8 * q + row, c + o, v, w, min(4, p.n - c - o));
-            }
-        } else {
-            const int row = lane >> 3, o = 4 * (lane & 7);
-            if (8 * q + row < rows) {
-                const f32x4 v = *(lds_f4*)((lds_f*)own + 32 * row + o);
-                finish<false>(p, m + 8 * q + row, c + o, v, v, min(4, p.n - c - o));
-            }
-        }
+        float v[V], w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = get[i], w[i] = GATED ? get[16 + i] : 0.f;
         wave_lds_order();
+        if (8 * q + row < rows) finish<GATED, V>(p, m + 8 * q + row, c + o, v, w, min(V, p.n - c - o));
     }
 }
 
@@ -175,14 +175,20 @@ __global__ __launch_bounds__(256) void linear_reduce(const Linear p, const float
     const int64_t m = (tt % mtiles) * BM + row;
     const int c = (int)(nt0 + tt / mtiles) * OUT + o;
     if (m >= p.a.M || c >= p.n) return;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
     const float* q = part + (size_t)tt * ksplit * (BM * BN) + row * BN + (GATED ? 32 * (o >> 4) + (o & 15) : o);
-    f32x4 v = *reinterpret_cast<const f32x4*>(q), w = v;
-    if (GATED) w = *reinterpret_cast<const f32x4*>(q + 16);
-    for (int k = 1; k < ksplit; ++k) {
-        v += *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN));
-        if (GATED) w += *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN) + 16);
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < ksplit; ++k) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += x[i];
+        if (GATED) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(q + (size_t)k * (BM * BN) + 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] += y[i];
+        }
     }
-    finish<GATED>(p, m, c, v, w, min(4, p.n - c));
+    finish<GATED, 4>(p, m, c, v, w, min(4, p.n - c));
 }
 
 // cols == 0: the sums are of nothing.
@@ -191,9 +197,10 @@ __global__ __launch_bounds__(256) void linear_of_nothing(const Linear p, int64_t
     if (e >= outputs) return;
     const int64_t m = e / p.n;
     const int c = (int)(e - m * p.n);
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (p.a.gated) finish<true>(p, m, c, zero, zero, 1);
-    else finish<false>(p, m, c, zero, zero, 1);
+    float v[2] = {0.f, 0.f};
+    const float w[2] = {0.f, 0.f};
+    if (p.a.gated) finish<true, 2>(p, m, c, v, w, 1);
+    else finish<false, 2>(p, m, c, v, w, 1);
 }
 
 // Tiles and what is split.  Up to 256 rows all tiles are split alike, so that the
