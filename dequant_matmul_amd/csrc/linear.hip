@@ -8,103 +8,11 @@
 // second launch adds them in order and applies the epilogue.
 #include <algorithm>
 
-#include "activation.h"
-#include "fqm_layer.h"
+#include "linear.h"
 #include "lut_gemm_tile.h"
 
 namespace fqm {
 namespace {
-
-// What every workgroup needs of a call.
-struct Linear {
-    fqm_epilogue a;
-    const uint8_t* packed;
-    int64_t ld;
-    const uint16_t* lut;
-    int N, K;  // rows and columns of W
-    int n;     // columns of Y
-};
-
-// Tile columns of the two stacked matrices: block b of 32 holds outputs n0 + 16 b
-// .. + 15, the first matrix's rows in columns 0..15, the second's in 16..31.
-struct StackedRows {
-    int n, n0;
-    __device__ __forceinline__ int output(int r) const { return n0 + 16 * (r >> 5) + (r & 15); }
-    __device__ __forceinline__ bool has(int r) const { return output(r) < n; }
-    __device__ __forceinline__ int row(int r) const { return min(output(r), n - 1) + (r >> 4 & 1) * n; }
-};
-
-// V values (2 or 4) at their element's alignment (gfx950's global accesses take any).
-template <int V>
-struct Values {
-    typedef float f32 __attribute__((ext_vector_type(V)));
-    typedef f32 f32_at __attribute__((aligned(4)));
-    typedef uint16_t u16 __attribute__((ext_vector_type(V)));
-    typedef u16 u16_at __attribute__((aligned(2)));
-};
-
-__device__ __forceinline__ float load_value(const void* p, int dtype, int64_t at) {
-    return dtype == FQM_F32 ? static_cast<const float*>(p)[at] : bf16_to_f32(static_cast<const uint16_t*>(p)[at]);
-}
-// n of them, the others 0
-template <int V>
-__device__ __forceinline__ void load_values(const void* p, int dtype, int64_t at, int n, float (&v)[V]) {
-    if (n == V && dtype == FQM_F32) {
-        const auto q = *reinterpret_cast<const typename Values<V>::f32_at*>(static_cast<const float*>(p) + at);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = q[i];
-    } else if (n == V) {
-        const auto q = *reinterpret_cast<const typename Values<V>::u16_at*>(static_cast<const uint16_t*>(p) + at);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = bf16_to_f32(q[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = i < n ? load_value(p, dtype, at + i) : 0.f;
-    }
-}
-template <int V>
-__device__ __forceinline__ void store_values(void* p, int dtype, int64_t at, const float (&v)[V], int n) {
-    typename Values<V>::u16 h;
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-    float* pf = static_cast<float*>(p) + at;
-    uint16_t* ph = static_cast<uint16_t*>(p) + at;
-    if (n == V && dtype == FQM_F32) {
-        typename Values<V>::f32 q;
-#pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = v[i];
-        *reinterpret_cast<typename Values<V>::f32_at*>(pf) = q;
-    } else if (n == V) {
-        *reinterpret_cast<typename Values<V>::u16_at*>(ph) = h;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) {
-                if (dtype == FQM_F32) pf[i] = v[i];
-                else ph[i] = h[i];
-            }
-    }
-}
-
-// Outputs c .. c + V - 1 of row m (n of them) from their sums v, and w of the second matrix.
-template <bool GATED, int V>
-__device__ __forceinline__ void finish(const Linear& p, int64_t m, int c, float (&v)[V], const float (&w)[V], int n) {
-    const fqm_epilogue& a = p.a;
-    if (n <= 0) return;
-    float b[V], wb[V], r[V];
-    if (a.residual) load_values<V>(a.residual, a.res_dtype, m * a.ld_res + c, n, r);
-    if (a.bias) {
-        load_values<V>(a.bias, a.bias_dtype, c, n, b);
-        if (GATED) load_values<V>(a.bias, a.bias_dtype, p.n + c, n, wb);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        v[i] = activate(a.act, a.bias ? v[i] + b[i] : v[i]);
-        if (GATED) v[i] *= a.bias ? w[i] + wb[i] : w[i];
-        if (a.residual) v[i] += r[i];
-    }
-    store_values<V>(a.Y, a.y_dtype, m * a.ld_y + c, v, n);
-}
 
 typedef __attribute__((address_space(3))) float lds_f;
 
@@ -191,6 +99,319 @@ __global__ __launch_bounds__(256) void linear_reduce(const Linear p, const float
     finish<GATED, 4>(p, m, c, v, w, min(4, p.n - c));
 }
 
+// ---- up to 32 rows -----------------------------------------------------------------------
+// Here the weights' stream is the work.  A workgroup's 4 waves own 32 rows of W each and share the
+// rows of X; K goes by in stages of 128.  Codes and X come by direct global -> LDS loads, two stages
+// ahead in a ring of three, in whole 64-byte pieces of a row: read straight into the operands' layout
+// (24 bytes a lane, a row of W on every second lane) the codes cost the address unit 128 accesses for 2 KB
+// and bound the kernel at 28 us for 69 MB; this way they cost 24.
+//
+// All tiles' stages are one range, cut evenly over the workgroups (two a compute unit): each has the same
+// work whatever the shape, and at most two tiles that it shares with others.  Their sums go through the
+// workspace, and a second launch adds them in order and applies the epilogue.
+//
+// LDS layouts, chunks of 16 bytes.  Codes: 6 (6-bit) or 4 chunks a row, a row's chunks turned (6) or XORed (4)
+// by its number so that the 64 lanes' reads (row j, half g) meet every bank equally.  X: 16 chunks a row, XORed
+// by row % 16.
+constexpr int kStreamRows = 32;
+constexpr int kStreamWaves = 4;
+constexpr int kRing = 2;
+
+// Workgroup g's first stage of all tiles' `total`, and the workgroup that has stage u (32 bits hold total * groups).
+__device__ __forceinline__ uint32_t stream_first(uint32_t g, uint32_t total, uint32_t groups) { return g * total / groups; }
+__device__ __forceinline__ uint32_t stream_owner(uint32_t u, uint32_t total, uint32_t groups) {
+    return ((u + 1) * groups - 1) / total;
+}
+
+template <int BITS, int MX, bool GATED>
+__device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* __restrict__ part) {
+    using F = GemmFmt<BITS>;
+    constexpr int NW = kStreamWaves, ND = F::ND, OUT = GATED ? 16 : 32, BN = 32 * NW;
+    constexpr int MB = (MX + 1) / 2;                  // 32-row blocks of X
+    constexpr int CH = BITS == 6 ? 6 : 4;             // chunks of a row's codes per stage
+    constexpr int CD = CH / 2;                        // 1 KB loads of a wave's codes per stage
+    constexpr int PER = CD + MX;                      // loads of a wave per stage
+    __shared__ __attribute__((aligned(8192))) uint8_t s_tab[(NW / 2) * F::PLANE];
+    __shared__ __attribute__((aligned(16))) uint8_t s_zero[16];
+    // objects of their own, so that the compiler sees which reads a load under way does not concern
+    __shared__ __attribute__((aligned(16))) uint8_t s_c0[NW * 1024 * CD];
+    __shared__ __attribute__((aligned(16))) uint8_t s_c1[NW * 1024 * CD];
+    __shared__ __attribute__((aligned(16))) uint8_t s_c2[kRing > 2 ? NW * 1024 * CD : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x0[MX * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x1[MX * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x2[kRing > 2 ? MX * 4096 : 16];
+    lds8* const CS[3] = {(lds8*)s_c0, (lds8*)s_c1, (lds8*)s_c2};
+    lds8* const XS[3] = {(lds8*)s_x0, (lds8*)s_x1, (lds8*)s_x2};
+    const fqm_epilogue& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int M = (int)a.M, ksteps = p.K / BK, stages = (ksteps + 1) / 2;
+    const int total = tiles * stages;
+    const int u0 = (int)stream_first(blockIdx.x, total, gridDim.x), u1 = (int)stream_first(blockIdx.x + 1, total, gridDim.x);
+
+    // X: load u of wave w fills rows 4 (MX w + u) .. + 3, lane l the place l % 16 of row l / 16
+    const __amdgpu_buffer_rsrc_t xrsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.X, (short)0, 0x7fffffff, 0x00020000);
+    uint32_t xrow[MX], xin[MX];
+#pragma unroll
+    for (int u = 0; u < MX; ++u) {
+        const int row = 4 * (MX * wave + u) + (lane >> 4);
+        xrow[u] = (uint32_t)min(row, M - 1) * (uint32_t)a.ld_x * 2u;
+        xin[u] = 16u * ((lane & 15) ^ (row & 15));
+    }
+    // operand reads: row j (+ 32), logical chunk 8 h + 4 g + q
+    int aoff[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) aoff[c] = 256 * j + 16 * ((8 * (c >> 2) + 4 * g + (c & 3)) ^ (j & 15));
+    // code reads of lane (j, g): its 24 (16) bytes of both steps of a stage
+    constexpr int CR = BITS == 6 ? 6 : 2;
+    int coff[CR];
+#pragma unroll
+    for (int i = 0; i < CR; ++i) {
+        if constexpr (BITS == 6) {
+            const int at = 48 * (i / 3) + 24 * g + 8 * (i % 3);  // byte of the row's 96
+            coff[i] = 96 * j + 16 * ((at / 16 + (j >> 3)) % 6) + (at & 15);
+        } else {
+            coff[i] = 64 * j + 16 * ((2 * i + g) ^ ((j >> 2) & 3));
+        }
+    }
+    uint32_t cmask = (uint32_t)(F::ENTRIES - 1) << 7;
+    asm volatile("" : "+v"(cmask));  // in a VGPR: (v & mask) | base is one v_and_or_b32
+    const uint32_t tbase = (uint32_t)F::PLANE * (wave >> 1) + 4u * j + 2u * (wave & 1);
+    lds8* const TAB = (lds8*)s_tab;
+
+    for (int u = u0; u < u1;) {
+        const int nt = u / stages, s0 = u - nt * stages, s1 = min(stages, s0 + (u1 - u));
+        const auto wr = [&] {
+            if constexpr (GATED) return StackedRows{p.n, OUT * NW * nt};
+            else return RunOfRows{p.N, BN * nt};
+        }();
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): from here on only the loads below are counted
+        __syncthreads();                     // every wave is done with the last tile's LDS
+        // codes: load u of a wave fills 64 chunks, in order of (row, place)
+        const uint8_t* base = p.packed + (int64_t)wr.row(32 * wave) * p.ld;
+        const __amdgpu_buffer_rsrc_t crsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7fffffff, 0x00020000);
+        uint32_t crow[CD], cin[CD];
+#pragma unroll
+        for (int v = 0; v < CD; ++v) {
+            const int e = 64 * v + lane, row = e / CH, place = e - row * CH;
+            crow[v] = (uint32_t)((int64_t)(wr.row(32 * wave + row) - wr.row(32 * wave)) * p.ld);
+            cin[v] = 16u * (BITS == 6 ? (place + 6 - (row >> 3)) % 6 : place ^ ((row >> 2) & 3));
+        }
+        // past a row's end (the second half of a last stage, where K is an odd number of steps): a chunk of codes
+        // again, and for X an offset past the buffer, which loads zeros
+        const uint32_t clast = (uint32_t)(F::STEP_BYTES * ksteps - 16), xend = 2u * (uint32_t)p.K;
+        auto load_stage = [&](int ring, int s) {
+#pragma unroll
+            for (int v = 0; v < CD; ++v)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(crsrc, (lvoid*)(CS[ring] + 1024 * (CD * wave + v)), 16,
+                                                         crow[v] + min(cin[v] + (uint32_t)s * (16u * CH), clast), 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < MX; ++v) {
+                const uint32_t at = xin[v] + (uint32_t)s * 256u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xrsrc, (lvoid*)(XS[ring] + 1024 * (MX * wave + v)), 16,
+                                                         at < xend ? xrow[v] + at : 0xffffff00u, 0, 0, 0);
+            }
+        };
+        // tables, bank-sliced as in the tiles
+        {
+            constexpr int EPT = F::ENTRIES / 8;
+            uint32_t tv[BN * 8 / (64 * NW)][EPT / 2];
+#pragma unroll
+            for (int v = 0; v < BN * 8 / (64 * NW); ++v) {
+                const int i = tid + 64 * NW * v;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(p.lut + (int64_t)wr.row(i >> 3) * F::ENTRIES + EPT * (i & 7));
+                if constexpr (EPT == 8) {
+                    const u32x4 q = *reinterpret_cast<const u32x4*>(src);
+                    tv[v][0] = q[0], tv[v][1] = q[1], tv[v][2] = q[2], tv[v][3] = q[3];
+                } else {
+                    tv[v][0] = *src;
+                }
+            }
+            load_stage(0, s0);
+            if constexpr (kRing > 2) load_stage(1, min(s0 + 1, s1 - 1));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int v = 0; v < BN * 8 / (64 * NW); ++v) {
+                const int i = tid + 64 * NW * v, r = i >> 3;
+                lds8* dst = TAB + F::PLANE * (r >> 6) + 4 * (r & 31) + 2 * ((r >> 5) & 1) + 128 * EPT * (i & 7);
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) *(lds16*)(dst + 128 * e) = (uint16_t)(tv[v][e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        if (tid == 0) *(__attribute__((address_space(3))) uint32_t*)s_zero = 0u;
+
+        f32x16 acc[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+        uint32_t mask1 = cmask, base1 = tbase;
+        auto step = [&](auto rc, auto hc) {
+            constexpr int ring = decltype(rc)::value, h = decltype(hc)::value;
+            uint32_t cw[ND];
+            lds8* from = CS[ring] + 1024 * CD * wave;
+#pragma unroll
+            for (int i = 0; i < ND / 2; ++i) {
+                if constexpr (BITS == 6) {
+                    const u32x2 d = *(__attribute__((address_space(3))) const u32x2*)(from + coff[3 * h + i]);
+                    cw[2 * i] = d[0], cw[2 * i + 1] = d[1];
+                } else if (i == 0) {
+                    const u32x4 d = *(lds128c*)(from + coff[h]);
+                    cw[0] = d[0], cw[1] = d[1], cw[2] = d[2], cw[3] = d[3];
+                }
+            }
+            auto slice = [&](auto qc) {
+                constexpr int q = decltype(qc)::value;
+                uint32_t ad[8], wv[8];
+                if constexpr (h == 0) slice_addrs<BITS, q>(cw, cmask, tbase, ad);
+                else slice_addrs<BITS, q>(cw, mask1, base1, ad);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) wv[e] = *(lds16c*)(TAB + ad[e]);
+                u32x4 bw;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bw[e] = __builtin_amdgcn_perm(wv[2 * e + 1], wv[2 * e], 0x05040100u);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const bf16x8 x = __builtin_bit_cast(bf16x8, *(lds128c*)(XS[ring] + aoff[4 * h + q] + 8192 * i));
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, bw), acc[i], 0, 0, 0);
+                }
+            };
+            slice(Slice<0>{});
+            slice(Slice<1>{});
+            slice(Slice<2>{});
+            slice(Slice<3>{});
+        };
+        auto stage = [&](auto rc, int s) {
+            constexpr int R = decltype(rc)::value, R2 = (R + kRing - 1) % kRing;
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0070 | (PER * (kRing - 2)));  // vmcnt lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            load_stage(R2, min(s + kRing - 1, s1 - 1));
+            const bool none = 2 * s + 1 >= ksteps;  // no second half: its weights are the zero
+            mask1 = none ? 0u : cmask;
+            base1 = none ? (uint32_t)(uintptr_t)(lds8*)s_zero - (uint32_t)(uintptr_t)TAB : tbase;
+            step(rc, Slice<0>{});
+            step(rc, Slice<1>{});
+        };
+        int s = s0;
+        for (; s + kRing - 1 < s1; s += kRing) {
+            stage(Buf<0>{}, s);
+            stage(Buf<1>{}, s + 1);
+            if constexpr (kRing > 2) stage(Buf<kRing - 1>{}, s + 2);
+        }
+        if (s < s1) stage(Buf<0>{}, s);
+        if constexpr (kRing > 2) if (s + 1 < s1) stage(Buf<1>{}, s + 1);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may still be writing this workgroup's LDS
+        if (s0 == 0 && s1 == stages) {
+            __syncthreads();
+#pragma unroll 1
+            for (int i = 0; i < MB; ++i) {
+                f32x16 sums = acc[0];
+                if (MB > 1 && i == 1) sums = acc[MB - 1];
+                finish_block<GATED>(p, XS[0] + 1024 * wave, sums, 32 * i, OUT * (NW * nt + wave), M - 32 * i);
+            }
+        } else {
+            float* q = part + ((size_t)2 * blockIdx.x + (u != u0)) * M * BN + 32 * wave + j;
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = 32 * i + (r & 3) + 8 * (r >> 2) + 4 * g;
+                    if (row < M) q[(size_t)row * BN] = acc[i][r];
+                }
+        }
+        u += s1 - s0;
+    }
+}
+
+template <int BITS, int MX, bool GATED>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(const Linear p, int tiles, float* __restrict__ part) {
+    stream_tiles<BITS, MX, GATED>(p, tiles, part);
+}
+
+// Y of the tiles that workgroups share: their sums in order, then the epilogue.  Workgroup: 1024 outputs of a tile
+// at most, 4 a thread.
+template <bool GATED>
+__global__ __launch_bounds__(256) void linear_stream_sum(const Linear p, const float* __restrict__ part, int tiles, int groups,
+                                                         int per_tile) {
+    constexpr int BN = 32 * kStreamWaves, OUT = GATED ? BN / 2 : BN, AT_ONCE = 4;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    const int nt = blockIdx.x / per_tile, e = (blockIdx.x - nt * per_tile) * 256 + threadIdx.x;
+    const int M = (int)p.a.M, m = e / (OUT / 4), o = 4 * (e % (OUT / 4)), c = OUT * nt + o;
+    const uint32_t stages = (uint32_t)(p.K / BK + 1) / 2, total = tiles * stages, lo = nt * stages;
+    const int g0 = (int)stream_owner(lo, total, groups), g1 = (int)stream_owner(lo + stages - 1, total, groups);
+    if (g0 == g1 || m >= M || c >= p.n) return;  // g0 == g1: that workgroup has finished the tile
+    const bool later = stream_first(g0, total, groups) < lo;  // g0's second place: its last tile
+    const float* q = part + (size_t)m * BN + (GATED ? 32 * (o >> 4) + (o & 15) : o);
+    const size_t each = (size_t)M * BN;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = g0; g <= g1; g += AT_ONCE) {
+        f32x4 x[AT_ONCE], y[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const float* from = q + each * (2 * min(g + k, g1) + (g + k == g0 && later));
+            x[k] = *reinterpret_cast<const f32x4*>(from);
+            if (GATED) y[k] = *reinterpret_cast<const f32x4*>(from + 16);
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] += g + k <= g1 ? x[k][i] : 0.f;
+                if (GATED) w[i] += g + k <= g1 ? y[k][i] : 0.f;
+            }
+    }
+    finish<GATED, 4>(p, m, c, v, w, min(4, p.n - c));
+}
+
+// Of the current device (without one, an MI355X's).
+int compute_units() {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    return std::max(cus, 1);
+}
+
+struct StreamPlan {
+    int tiles, groups;
+    bool shared;  // whether some tile is
+    size_t part_bytes;
+};
+
+StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, bool gated) {
+    StreamPlan p;
+    const int64_t n = gated ? N / 2 : N, per = (gated ? 16 : 32) * kStreamWaves, stages = (K / BK + 1) / 2;
+    p.tiles = (int)((n + per - 1) / per);
+    const int64_t total = p.tiles * stages;
+    p.groups = (int)std::min<int64_t>(2 * compute_units(), (total + 3) / 4);
+    p.shared = total % p.groups || total / p.groups % stages;
+    p.part_bytes = p.shared ? (size_t)2 * p.groups * M * 32 * kStreamWaves * 4 : 0;
+    return p;
+}
+
+template <int BITS, int MX, bool GATED>
+hipError_t launch_stream(const Linear& p, float* part, hipStream_t s) {
+    const StreamPlan plan = stream_plan(p.N, p.K, p.a.M, GATED);
+    hipLaunchKernelGGL((linear_stream_kernel<BITS, MX, GATED>), dim3((unsigned)plan.groups), dim3(64 * kStreamWaves), 0, s, p,
+                       plan.tiles, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !plan.shared) return e;
+    const int per_tile = ((int)p.a.M * (GATED ? 4 : 8) * kStreamWaves + 255) / 256;
+    hipLaunchKernelGGL(linear_stream_sum<GATED>, dim3((unsigned)(plan.tiles * per_tile)), dim3(256), 0, s, p, part, plan.tiles,
+                       plan.groups, per_tile);
+    return hipGetLastError();
+}
+
+// The loads' 32-bit offsets reach both matrices of a tile, and the stages are counted in 32 bits.
+bool stream_path(const Linear& p) {
+    const StreamPlan plan = stream_plan(p.N, p.K, p.a.M, p.a.gated);
+    return p.a.M <= kStreamRows && (p.a.gated ? (int64_t)(p.n + 32) * p.ld : 32 * p.ld) < 0x7fffffff &&
+           (int64_t)plan.tiles * ((p.K / BK + 1) / 2 + 1) * plan.groups <= 0x7fffffff;
+}
+
 // cols == 0: the sums are of nothing.
 __global__ __launch_bounds__(256) void linear_of_nothing(const Linear p, int64_t outputs) {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -214,16 +435,6 @@ struct LinearPlan {
     int64_t tail;     // the others
     size_t part_bytes;
 };
-
-// Of the current device (without one, an MI355X's).
-int compute_units() {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
-        (void)hipGetLastError();
-        return 256;
-    }
-    return std::max(cus, 1);
-}
 
 LinearPlan linear_plan(int64_t N, int64_t K, int64_t M, bool gated) {
     LinearPlan p;
@@ -274,21 +485,21 @@ hipError_t launch_tiles(const Linear& p, const LinearPlan& plan, float* part, hi
 }
 
 template <int BITS, bool GATED>
-hipError_t launch_bits(const Linear& p, void* ws, hipStream_t s) {
-    const LinearPlan plan = linear_plan(p.N, p.K, p.a.M, GATED);
+hipError_t launch_tile_bits(const Linear& p, void* ws, hipStream_t s) {
     float* part = static_cast<float*>(ws);
+    const LinearPlan plan = linear_plan(p.N, p.K, p.a.M, GATED);
     if (plan.bm == 32) return launch_tiles<BITS, 32, 4, GATED>(p, plan, part, s);
     if (plan.bm == 64) return launch_tiles<BITS, 64, 4, GATED>(p, plan, part, s);
     return launch_tiles<BITS, 256, 8, GATED>(p, plan, part, s);
 }
 
-}  // namespace
-
-size_t linear_workspace(const fqm_weights& w, const fqm_epilogue& a) {
-    return w.cols == 0 ? 0 : linear_plan(w.rows, w.cols, a.M, a.gated).part_bytes;
+template <int BITS, bool GATED>
+hipError_t launch_stream_bits(const Linear& p, void* ws, hipStream_t s) {
+    float* part = static_cast<float*>(ws);
+    return p.a.M <= 16 ? launch_stream<BITS, 1, GATED>(p, part, s) : launch_stream<BITS, 2, GATED>(p, part, s);
 }
 
-hipError_t launch_linear(const fqm_weights& w, const fqm_epilogue& a, void* ws, hipStream_t s) {
+Linear linear_of(const fqm_weights& w, const fqm_epilogue& a) {
     Linear p;
     p.a = a;
     const bool six = w.format == FQM_LUT6;
@@ -298,14 +509,47 @@ hipError_t launch_linear(const fqm_weights& w, const fqm_epilogue& a, void* ws, 
     p.N = (int)w.rows;
     p.K = (int)w.cols;
     p.n = a.gated ? p.N / 2 : p.N;
+    return p;
+}
+
+enum class Path { rows, mfma, stream, tiles };
+Path path_of(const fqm_weights& w, const Linear& p) {
+    if (p.a.M <= 3 && (w.format == FQM_LUT6 ? lut6_gemv_rows_path(w, (int)p.a.M) : lut4_gemv_rows_path(w, (int)p.a.M))) return Path::rows;
+    if (p.a.M <= 8 && lut_gemv_mfma_supported(w, (int)std::max<int64_t>(p.a.M, 2))) return Path::mfma;
+    return stream_path(p) ? Path::stream : Path::tiles;
+}
+}  // namespace
+
+size_t linear_workspace(const fqm_weights& w, const fqm_epilogue& a) {
+    if (w.cols == 0) return 0;
+    const Linear p = linear_of(w, a);
+    switch (path_of(w, p)) {
+        case Path::rows: return 0;
+        case Path::mfma: return lut_linear_mfma_workspace(p);
+        case Path::stream: return stream_plan(p.N, p.K, a.M, a.gated).part_bytes;
+        default: return linear_plan(p.N, p.K, a.M, a.gated).part_bytes;
+    }
+}
+
+hipError_t launch_linear(const fqm_weights& w, const fqm_epilogue& a, void* ws, hipStream_t s) {
+    const Linear p = linear_of(w, a);
     if (p.K == 0) {
         const int64_t outputs = a.M * p.n, grid = (outputs + 255) / 256;
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
         hipLaunchKernelGGL(linear_of_nothing, dim3((unsigned)grid), dim3(256), 0, s, p, outputs);
         return hipGetLastError();
     }
-    if (six) return a.gated ? launch_bits<6, true>(p, ws, s) : launch_bits<6, false>(p, ws, s);
-    return a.gated ? launch_bits<4, true>(p, ws, s) : launch_bits<4, false>(p, ws, s);
+    const bool six = w.format == FQM_LUT6;
+    switch (path_of(w, p)) {
+        case Path::rows: return six ? launch_lut6_linear(p, s) : launch_lut4_linear(p, s);
+        case Path::mfma: return launch_lut_linear_mfma(p, six, static_cast<float*>(ws), s);
+        case Path::stream:
+            if (six) return a.gated ? launch_stream_bits<6, true>(p, ws, s) : launch_stream_bits<6, false>(p, ws, s);
+            return a.gated ? launch_stream_bits<4, true>(p, ws, s) : launch_stream_bits<4, false>(p, ws, s);
+        default:
+            if (six) return a.gated ? launch_tile_bits<6, true>(p, ws, s) : launch_tile_bits<6, false>(p, ws, s);
+            return a.gated ? launch_tile_bits<4, true>(p, ws, s) : launch_tile_bits<4, false>(p, ws, s);
+    }
 }
 
 }  // namespace fqm

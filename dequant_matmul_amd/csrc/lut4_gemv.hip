@@ -10,13 +10,12 @@
 // Codes are two per byte (code 2j in the low nibble of byte j), so a row of
 // 1024 weights is 512 bytes: half the bytes of the 6-bit format for the same
 // decode work per weight.
-#include "fqm_internal.h"
+#include "gemv_rows_out.h"
 
 namespace fqm {
 namespace {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) const uint16_t lds_u16;
 typedef __attribute__((address_space(3))) const uint32_t lds_u32c;
@@ -58,25 +57,22 @@ __device__ __forceinline__ uint32_t code4_x2(uint32_t d0, uint32_t d1) {
 // five table loads and four LDS stores per lane and row, which only rows of
 // many cells repay.
 // ---------------------------------------------------------------------------
-template <int CPR, int WPG, int PC, bool PT>
-__global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells(const uint8_t* __restrict__ packed, int64_t ld,
-                                                            const uint16_t* __restrict__ lut,
-                                                            const uint16_t* __restrict__ x,
-                                                            void* __restrict__ y, int y_f32, int rows) {
+template <int CPR, int WPG, int PC, bool PT, class Out>
+__device__ __forceinline__ void gemv_cells(const uint8_t* __restrict__ packed, int64_t ld, const uint16_t* __restrict__ lut,
+                                           const Out& out) {
     constexpr int NX = CPR * 128;                          // x in 16-byte pieces
     constexpr int XS = (NX + 64 * WPG - 1) / (64 * WPG);   // staging pieces per thread
     __shared__ __attribute__((aligned(16))) u32x4_t s_x[NX];
     __shared__ __attribute__((aligned(PT ? 1024 : 32))) uint32_t s_tab[WPG][PT ? 256 : 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row_u = blockIdx.x * WPG + wv;
-    const int row = min(row_u, rows - 1);  // rows past the end repeat the last row (not stored)
+    const int row = out.row(blockIdx.x, wv, WPG);  // rows past the end repeat the last row (not stored)
     const uint8_t* rowp = packed + (int64_t)row * ld + 8 * lane;
 
     u32x4_t xs[XS];
 #pragma unroll
     for (int u = 0; u < XS; ++u)
-        xs[u] = reinterpret_cast<const u32x4_t*>(x)[min(tid + u * 64 * WPG, NX - 1)];
+        xs[u] = out.template x_piece<NX>(min(tid + u * 64 * WPG, NX - 1));
     const uint16_t* lr = lut + (int64_t)row * 16;
     const uint32_t tv = PT ? (uint32_t)lr[lane & 15] : reinterpret_cast<const uint32_t*>(lr)[lane & 7];
     uint32_t t_hi[4];  // PT: entries (lane >> 4) + 4 t, the high halves of pairs lane + 64 t
@@ -163,13 +159,18 @@ __global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells(const uint8_t* __res
             acc1 = dot2(w1, xv[j + 1], acc1);
         }
     }
-    const float sum = wave_sum_lane63(acc0 + acc1);
-    if (lane == 63 && row_u < rows) {
-        if (y_f32)
-            reinterpret_cast<float*>(y)[row_u] = sum;
-        else
-            reinterpret_cast<uint16_t*>(y)[row_u] = f32_to_bf16(sum);
-    }
+    __shared__ float s_sum[WPG][1];
+    const float sum[1] = {wave_sum_lane63(acc0 + acc1)};
+    out.template done<WPG, 1>(blockIdx.x, wv, sum, s_sum);
+}
+template <int CPR, int WPG, int PC, bool PT>
+__global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells(const uint8_t* __restrict__ packed, int64_t ld,
+                                                            const uint16_t* __restrict__ lut, const PlainOut out) {
+    gemv_cells<CPR, WPG, PC, PT>(packed, ld, lut, out);
+}
+template <int CPR, int WPG, int PC, bool PT>
+__global__ __launch_bounds__(64 * WPG) void lut4_linear_cells(const LinearOut out) {
+    gemv_cells<CPR, WPG, PC, PT>(out.p.packed, out.p.ld, out.p.lut, out);
 }
 
 // Batches 2 and 3: the batch-1 structure with every batch row's x block in
@@ -178,25 +179,22 @@ __global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells(const uint8_t* __res
 // rows.  Every chunk ends in a scheduling barrier and passes the sums through
 // an empty asm, so the compiler cannot sink the dot2 chains to the final
 // reduction (that kept every chunk's operands live).
-template <int CPR, int WPG, int PC, int B>
-__global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells_batch(const uint8_t* __restrict__ packed, int64_t ld,
-                                                                  const uint16_t* __restrict__ lut,
-                                                                  const uint16_t* __restrict__ x,
-                                                                  void* __restrict__ y, int y_f32, int rows) {
+template <int CPR, int WPG, int PC, int B, class Out>
+__device__ __forceinline__ void gemv_cells_batch(const uint8_t* __restrict__ packed, int64_t ld,
+                                                 const uint16_t* __restrict__ lut, const Out& out) {
     constexpr int NX = CPR * 128;                              // x of one batch row in 16-byte pieces
     constexpr int XS = (B * NX + 64 * WPG - 1) / (64 * WPG);   // staging pieces per thread
     __shared__ __attribute__((aligned(16))) u32x4_t s_x[B * NX];
     __shared__ __attribute__((aligned(32))) uint32_t s_tab[WPG][8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row_u = blockIdx.x * WPG + wv;
-    const int row = min(row_u, rows - 1);  // rows past the end repeat the last row (not stored)
+    const int row = out.row(blockIdx.x, wv, WPG);  // rows past the end repeat the last row (not stored)
     const uint8_t* rowp = packed + (int64_t)row * ld + 8 * lane;
 
     u32x4_t xs[XS];
 #pragma unroll
     for (int u = 0; u < XS; ++u)
-        xs[u] = reinterpret_cast<const u32x4_t*>(x)[min(tid + u * 64 * WPG, B * NX - 1)];
+        xs[u] = out.template x_piece<NX>(min(tid + u * 64 * WPG, B * NX - 1));
     const uint32_t tv = reinterpret_cast<const uint32_t*>(lut + (int64_t)row * 16)[lane & 7];
     __builtin_amdgcn_sched_barrier(0);
 
@@ -265,16 +263,20 @@ __global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells_batch(const uint8_t*
         }
         __builtin_amdgcn_sched_barrier(0);
     }
+    __shared__ float s_sum[WPG][B];
+    float sum[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-        const float sum = wave_sum_lane63(acc0[b] + acc1[b]);
-        if (lane == 63 && row_u < rows) {
-            if (y_f32)
-                reinterpret_cast<float*>(y)[(int64_t)b * rows + row_u] = sum;
-            else
-                reinterpret_cast<uint16_t*>(y)[(int64_t)b * rows + row_u] = f32_to_bf16(sum);
-        }
-    }
+    for (int b = 0; b < B; ++b) sum[b] = wave_sum_lane63(acc0[b] + acc1[b]);
+    out.template done<WPG, B>(blockIdx.x, wv, sum, s_sum);
+}
+template <int CPR, int WPG, int PC, int B>
+__global__ __launch_bounds__(64 * WPG) void lut4_gemv_cells_batch(const uint8_t* __restrict__ packed, int64_t ld,
+                                                                  const uint16_t* __restrict__ lut, const PlainOut out) {
+    gemv_cells_batch<CPR, WPG, PC, B>(packed, ld, lut, out);
+}
+template <int CPR, int WPG, int PC, int B>
+__global__ __launch_bounds__(64 * WPG) void lut4_linear_cells_batch(const LinearOut out) {
+    gemv_cells_batch<CPR, WPG, PC, B>(out.p.packed, out.p.ld, out.p.lut, out);
 }
 
 // Any width (cols % 16 == 0) and batch 1..16: one row per wave, lane i takes
@@ -349,7 +351,7 @@ hipError_t launch_cells(const fqm_weights& w, const uint16_t* x, void* y, int y_
         // pair tables on rows of more than 8 cells: 5120 x 17408 took 14.4-14.6 us
         // against 15.2-15.4 us; on 17408 x 5120 they cost 8 % (14.9-15.0 against 13.8 us)
         hipLaunchKernelGGL((lut4_gemv_cells<CPR, WPG, 4, (CPR > 8)>), dim3(grid), dim3(64 * WPG), 0, s, w.lut4.packed,
-                           w.lut4.ld, w.lut4.lut, x, y, y_f32, (int)w.rows);
+                           w.lut4.ld, w.lut4.lut, PlainOut{x, y, y_f32, (int)w.rows});
         return hipGetLastError();
     }
 }
@@ -368,7 +370,7 @@ hipError_t launch_cells_batch(const fqm_weights& w, const uint16_t* x, void* y, 
         constexpr int WPG = CPR <= 8 ? 4 : 10;
         const unsigned grid = (unsigned)((w.rows + WPG - 1) / WPG);
         hipLaunchKernelGGL((lut4_gemv_cells_batch<CPR, WPG, 4, B>), dim3(grid), dim3(64 * WPG), 0, s,
-                           w.lut4.packed, w.lut4.ld, w.lut4.lut, x, y, y_f32, (int)w.rows);
+                           w.lut4.packed, w.lut4.ld, w.lut4.lut, PlainOut{x, y, y_f32, (int)w.rows});
         return hipGetLastError();
     }
 }
@@ -391,7 +393,32 @@ hipError_t launch_batch(const fqm_weights& w, const uint16_t* x, void* y, int y_
     }
 }
 
+// The same kernels with fqm_linear's epilogue, at the workgroup sizes of the plain ones.
+template <int CPR, int B>
+hipError_t launch_linear_cells(const Linear& p, hipStream_t s) {
+    if constexpr (CPR > (B == 1 ? kMaxCells : batch_max_cells(B))) {
+        return hipErrorInvalidValue;
+    } else {
+        if ((p.K >> 10) != CPR) return launch_linear_cells<CPR + 1, B>(p, s);
+        constexpr int WPG = CPR <= 8 ? 4 : 10;
+        const int per = p.a.gated ? WPG / 2 : WPG;
+        const unsigned grid = (unsigned)((p.n + per - 1) / per);
+        if constexpr (B == 1)
+            hipLaunchKernelGGL((lut4_linear_cells<CPR, WPG, 4, (CPR > 8)>), dim3(grid), dim3(64 * WPG), 0, s, LinearOut{p});
+        else
+            hipLaunchKernelGGL((lut4_linear_cells_batch<CPR, WPG, 4, B>), dim3(grid), dim3(64 * WPG), 0, s, LinearOut{p});
+        return hipGetLastError();
+    }
+}
+
 }  // namespace
+
+hipError_t launch_lut4_linear(const Linear& p, hipStream_t s) {
+    if (p.a.M == 1) return launch_linear_cells<1, 1>(p, s);
+    if (p.a.M == 2) return launch_linear_cells<1, 2>(p, s);
+    if (p.a.M == 3) return launch_linear_cells<1, 3>(p, s);
+    return hipErrorInvalidValue;
+}
 
 static bool cells_supported(const fqm_weights& w) {
     return w.cols > 0 && (w.cols & 1023) == 0 && (w.cols >> 10) <= kMaxCells;

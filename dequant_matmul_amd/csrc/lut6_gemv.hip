@@ -10,7 +10,7 @@
 // row's 128-byte table in LDS (one table per wave: the 64 lanes gather from
 // the same 32 banks without conflicts), and reduces its per-lane partial sums
 // across the wave at the end of the row.
-#include "fqm_internal.h"
+#include "gemv_rows_out.h"
 
 namespace fqm {
 namespace {
@@ -74,7 +74,6 @@ __global__ __launch_bounds__(256) void lut6_gemv_generic(const uint8_t* __restri
 }
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) const uint16_t lds_u16;
 typedef __attribute__((address_space(3))) const u32x4_t lds_u4;
@@ -118,13 +117,9 @@ __device__ __forceinline__ uint32_t code_x2(uint32_t d0, uint32_t d1, uint32_t d
 // S > 1 the S partials are added in wave order through LDS, so the result
 // does not depend on timing.
 // ---------------------------------------------------------------------------
-template <int CPR, int S, int WPG, int PC>
-__global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __restrict__ packed,
-                                                           int64_t ld,
-                                                           const uint16_t* __restrict__ lut,
-                                                           const uint16_t* __restrict__ x,
-                                                           void* __restrict__ y, int y_f32,
-                                                           int rows) {
+template <int CPR, int S, int WPG, int PC, class Out>
+__device__ __forceinline__ void gemv_rows(const uint8_t* __restrict__ packed, int64_t ld, const uint16_t* __restrict__ lut,
+                                          const Out& out) {
     constexpr int RPG = WPG / S;                           // rows per workgroup
     constexpr int NCH = (CPR + S - 1) / S;                 // most chunks per wave
     constexpr int NX = CPR * 128;                          // x in 16-byte pieces
@@ -135,8 +130,7 @@ __global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __rest
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int rr = wv / S, sp = wv - rr * S;   // row within the group, split index
-    const int row_u = blockIdx.x * RPG + rr;
-    const int row = min(row_u, rows - 1);  // rows past the end repeat the last row (not stored)
+    const int row = out.row(blockIdx.x, rr, RPG);  // rows past the end repeat the last row (not stored)
     const int cs = (sp * CPR) / S, n = ((sp + 1) * CPR) / S - cs;  // this wave's chunks [cs, cs + n)
     const uint8_t* rowp = packed + (int64_t)row * ld + 768 * cs + 12 * lane;
 
@@ -145,7 +139,7 @@ __global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __rest
     u32x4_t xs[XS];
 #pragma unroll
     for (int u = 0; u < XS; ++u)
-        xs[u] = reinterpret_cast<const u32x4_t*>(x)[min(tid + u * 64 * WPG, NX - 1)];
+        xs[u] = out.template x_piece<NX>(min(tid + u * 64 * WPG, NX - 1));
     const uint32_t tv = reinterpret_cast<const uint32_t*>(lut + (int64_t)row * 64)[lane & 31];
     __builtin_amdgcn_sched_barrier(0);
 
@@ -221,27 +215,28 @@ __global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __rest
         }
     }
     const float sum = wave_sum_lane63(acc0 + acc1);
+    __shared__ float s_sum[RPG][1];
     if (S == 1) {
-        if (lane == 63 && row_u < rows) {
-            if (y_f32)
-                reinterpret_cast<float*>(y)[row_u] = sum;
-            else
-                reinterpret_cast<uint16_t*>(y)[row_u] = f32_to_bf16(sum);
-        }
+        const float one[1] = {sum};
+        out.template done<RPG, 1>(blockIdx.x, rr, one, s_sum);
     } else {
         // the S partial sums of a row are added in wave order
         if (lane == 63) s_part[wv] = sum;
         __syncthreads();
-        if (sp == 0 && lane == 0 && row_u < rows) {
-            float t = s_part[wv];
+        float t[1] = {s_part[rr * S]};
 #pragma unroll
-            for (int q = 1; q < S; ++q) t += s_part[wv + q];
-            if (y_f32)
-                reinterpret_cast<float*>(y)[row_u] = t;
-            else
-                reinterpret_cast<uint16_t*>(y)[row_u] = f32_to_bf16(t);
-        }
+        for (int q = 1; q < S; ++q) t[0] += s_part[rr * S + q];
+        if (sp == 0) out.template done<RPG, 1>(blockIdx.x, rr, t, s_sum);
     }
+}
+template <int CPR, int S, int WPG, int PC>
+__global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __restrict__ packed, int64_t ld,
+                                                           const uint16_t* __restrict__ lut, const PlainOut out) {
+    gemv_rows<CPR, S, WPG, PC>(packed, ld, lut, out);
+}
+template <int CPR, int WPG, int PC>
+__global__ __launch_bounds__(64 * WPG) void lut6_linear_rows(const LinearOut out) {
+    gemv_rows<CPR, 1, WPG, PC>(out.p.packed, out.p.ld, out.p.lut, out);
 }
 
 // Batch rows B > 1 on the same layout: the workgroup stages B x blocks in LDS
@@ -250,27 +245,22 @@ __global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows(const uint8_t* __rest
 // all batch rows), and each wave reduces B row sums.  A scheduling barrier
 // closes every chunk and the sums are pinned there, so the unrolled loop
 // keeps one chunk's operands live at a time.
-template <int CPR, int WPG, int PC, int B>
-__global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows_batch(const uint8_t* __restrict__ packed,
-                                                                 int64_t ld,
-                                                                 const uint16_t* __restrict__ lut,
-                                                                 const uint16_t* __restrict__ x,
-                                                                 void* __restrict__ y, int y_f32,
-                                                                 int rows) {
+template <int CPR, int WPG, int PC, int B, class Out>
+__device__ __forceinline__ void gemv_rows_batch(const uint8_t* __restrict__ packed, int64_t ld,
+                                                const uint16_t* __restrict__ lut, const Out& out) {
     constexpr int NX = CPR * 128;                              // x of one batch row in 16-byte pieces
     constexpr int XS = (B * NX + 64 * WPG - 1) / (64 * WPG);   // staging pieces per thread
     __shared__ __attribute__((aligned(16))) u32x4_t s_x[B * NX];
     __shared__ __attribute__((aligned(16))) uint32_t s_tab[WPG][32];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row_u = blockIdx.x * WPG + wv;
-    const int row = min(row_u, rows - 1);  // rows past the end repeat the last row (not stored)
+    const int row = out.row(blockIdx.x, wv, WPG);  // rows past the end repeat the last row (not stored)
     const uint8_t* rowp = packed + (int64_t)row * ld + 12 * lane;
 
     u32x4_t xs[XS];
 #pragma unroll
     for (int u = 0; u < XS; ++u)
-        xs[u] = reinterpret_cast<const u32x4_t*>(x)[min(tid + u * 64 * WPG, B * NX - 1)];
+        xs[u] = out.template x_piece<NX>(min(tid + u * 64 * WPG, B * NX - 1));
     const uint32_t tv = reinterpret_cast<const uint32_t*>(lut + (int64_t)row * 64)[lane & 31];
     __builtin_amdgcn_sched_barrier(0);
 
@@ -343,16 +333,20 @@ __global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows_batch(const uint8_t* 
         }
         __builtin_amdgcn_sched_barrier(0);
     }
+    __shared__ float s_sum[WPG][B];
+    float sum[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-        const float sum = wave_sum_lane63(acc0[b] + acc1[b]);
-        if (lane == 63 && row_u < rows) {
-            if (y_f32)
-                reinterpret_cast<float*>(y)[(int64_t)b * rows + row_u] = sum;
-            else
-                reinterpret_cast<uint16_t*>(y)[(int64_t)b * rows + row_u] = f32_to_bf16(sum);
-        }
-    }
+    for (int b = 0; b < B; ++b) sum[b] = wave_sum_lane63(acc0[b] + acc1[b]);
+    out.template done<WPG, B>(blockIdx.x, wv, sum, s_sum);
+}
+template <int CPR, int WPG, int PC, int B>
+__global__ __launch_bounds__(64 * WPG) void lut6_gemv_rows_batch(const uint8_t* __restrict__ packed, int64_t ld,
+                                                                 const uint16_t* __restrict__ lut, const PlainOut out) {
+    gemv_rows_batch<CPR, WPG, PC, B>(packed, ld, lut, out);
+}
+template <int CPR, int WPG, int PC, int B>
+__global__ __launch_bounds__(64 * WPG) void lut6_linear_rows_batch(const LinearOut out) {
+    gemv_rows_batch<CPR, WPG, PC, B>(out.p.packed, out.p.ld, out.p.lut, out);
 }
 
 template <int CPR, int S, int WPG, int PC>
@@ -360,7 +354,7 @@ hipError_t launch_rows(const fqm_weights& w, const uint16_t* x, void* y, int y_f
     constexpr int RPG = WPG / S;
     const unsigned grid = (unsigned)((w.rows + RPG - 1) / RPG);
     hipLaunchKernelGGL((lut6_gemv_rows<CPR, S, WPG, PC>), dim3(grid), dim3(64 * WPG), 0, s,
-                       w.lut6.packed, w.lut6.ld, w.lut6.lut, x, y, y_f32, (int)w.rows);
+                       w.lut6.packed, w.lut6.ld, w.lut6.lut, PlainOut{x, y, y_f32, (int)w.rows});
     return hipGetLastError();
 }
 
@@ -420,7 +414,7 @@ hipError_t launch_cells_batch(const fqm_weights& w, const uint16_t* x, void* y, 
         constexpr int WPG = CPR <= 8 ? 4 : 10;
         const unsigned grid = (unsigned)((w.rows + WPG - 1) / WPG);
         hipLaunchKernelGGL((lut6_gemv_rows_batch<CPR, WPG, 4, B>), dim3(grid), dim3(64 * WPG), 0, s,
-                           w.lut6.packed, w.lut6.ld, w.lut6.lut, x, y, y_f32, (int)w.rows);
+                           w.lut6.packed, w.lut6.ld, w.lut6.lut, PlainOut{x, y, y_f32, (int)w.rows});
         return hipGetLastError();
     }
 }
@@ -432,7 +426,32 @@ hipError_t launch_rows_batch(const fqm_weights& w, const uint16_t* x, void* y, i
     return hipErrorInvalidValue;
 }
 
+// The same kernels with fqm_linear's epilogue, at the workgroup sizes of the plain ones.
+template <int CPR, int B>
+hipError_t launch_linear_cells(const Linear& p, hipStream_t s) {
+    if constexpr (CPR > (B == 1 ? kMaxCells : batch_max_cells(B))) {
+        return hipErrorInvalidValue;
+    } else {
+        if ((p.K >> 10) != CPR) return launch_linear_cells<CPR + 1, B>(p, s);
+        constexpr int WPG = CPR <= 8 ? 4 : 10;
+        const int per = p.a.gated ? WPG / 2 : WPG;
+        const unsigned grid = (unsigned)((p.n + per - 1) / per);
+        if constexpr (B == 1)
+            hipLaunchKernelGGL((lut6_linear_rows<CPR, WPG, 4>), dim3(grid), dim3(64 * WPG), 0, s, LinearOut{p});
+        else
+            hipLaunchKernelGGL((lut6_linear_rows_batch<CPR, WPG, 4, B>), dim3(grid), dim3(64 * WPG), 0, s, LinearOut{p});
+        return hipGetLastError();
+    }
+}
+
 }  // namespace
+
+hipError_t launch_lut6_linear(const Linear& p, hipStream_t s) {
+    if (p.a.M == 1) return launch_linear_cells<1, 1>(p, s);
+    if (p.a.M == 2) return launch_linear_cells<1, 2>(p, s);
+    if (p.a.M == 3) return launch_linear_cells<1, 3>(p, s);
+    return hipErrorInvalidValue;
+}
 
 bool lut6_gemv_rows_path(const fqm_weights& w, int batch) {
     return batch == 1 ? rows_supported(w) : rows_batch_supported(w, batch);

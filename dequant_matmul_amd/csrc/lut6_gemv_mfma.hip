@@ -37,7 +37,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "fqm_internal.h"
+#include "linear.h"
 
 namespace fqm {
 namespace {
@@ -115,12 +115,56 @@ __device__ __forceinline__ uint32_t tpos(uint32_t r, uint32_t q) {
     return r * 1024u + 16u * (q ^ sw);
 }
 
+// What becomes of a workgroup's sums: y as it is, fp32 parts where K is split, or fqm_linear's epilogue.  row(blk, r):
+// the row of W of row r of 16, some row past the end.
+struct PlainBlock {
+    void* y;
+    int y_f32, rows;
+    __device__ __forceinline__ int row(int blk, int r) const { return min(RB * blk + r, rows - 1); }
+    // v(r): the sum of row r of the 16; part: [batch][rows] of this K part, or NULL
+    template <class V>
+    __device__ __forceinline__ void done(int blk, int batch, float* part, V v) const {
+        const int r = threadIdx.x >> 4, col = threadIdx.x & 15, nr = RB * blk + r;
+        if (threadIdx.x >= RB * 16 || nr >= rows || col >= batch) return;
+        const float s = v(r);
+        if (part)
+            part[(int64_t)col * rows + nr] = s;
+        else if (y_f32)
+            reinterpret_cast<float*>(y)[(int64_t)col * rows + nr] = s;
+        else
+            reinterpret_cast<uint16_t*>(y)[(int64_t)col * rows + nr] = f32_to_bf16(s);
+    }
+};
+// With two stacked matrices 8 rows of each.
+struct LinearBlock {
+    const Linear p;
+    __device__ __forceinline__ OutputRows<RB> rows(int blk) const {
+        return {p.n, (p.a.gated ? RB / 2 : RB) * blk, p.a.gated};
+    }
+    __device__ __forceinline__ int row(int blk, int r) const { return rows(blk).row(r); }
+    template <class V>
+    __device__ __forceinline__ void done(int blk, int batch, float* part, V v) const {
+        const int r = threadIdx.x >> 4, col = threadIdx.x & 15, c = rows(blk).output(r);
+        if (threadIdx.x >= RB * 16 || c >= p.n || col >= batch) return;
+        if (part) {
+            part[(int64_t)col * p.N + row(blk, r)] = v(r);
+        } else if (!p.a.gated) {
+            float s[1] = {v(r)};
+            finish<false, 1>(p, col, c, s, s, 1);
+        } else if (r < RB / 2) {
+            float s[1] = {v(r)};
+            const float w[1] = {v(r + RB / 2)};
+            finish<true, 1>(p, col, c, s, w, 1);
+        }
+    }
+};
+
 // XROWS: batch rows an x block holds (8 or 16, >= batch); XPT = XROWS / 8
 // 16-byte x pieces per thread per chunk.
-template <int BITS, int XROWS>
+template <int BITS, int XROWS, class Out>
 __device__ __forceinline__ void gemv_mfma_body(
     const uint8_t* __restrict__ packed, int64_t ld, const uint16_t* __restrict__ lut,
-    const uint16_t* __restrict__ x, void* __restrict__ y, int y_f32, float* __restrict__ part,
+    const uint16_t* __restrict__ x, int64_t ld_x, const Out& out, float* __restrict__ part,
     int rows, int cols, int batch, int nblocks, int cps) {
     using F = LutFmt<BITS>;
     constexpr int PB = F::PB, ND = F::ND, CHB = F::CHB, CB_ROW = F::CB_ROW, TAB_BYTES = F::TAB_BYTES;
@@ -140,7 +184,6 @@ __device__ __forceinline__ void gemv_mfma_body(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int blk = blockIdx.x % nblocks, ks = blockIdx.x / nblocks;
-    const int n0 = blk * RB;
     const int nch = cols / CH;
     const int c0 = ks * cps, c1 = min(c0 + cps, nch);  // this workgroup's chunks [c0, c1)
     const int n = c1 - c0;
@@ -153,7 +196,7 @@ __device__ __forceinline__ void gemv_mfma_body(
     uint32_t tv[EPT / 2];
     {
         const uint32_t* tsrc =
-            reinterpret_cast<const uint32_t*>(lut + (int64_t)min(n0 + tr, rows - 1) * F::ENTRIES + tpart * EPT);
+            reinterpret_cast<const uint32_t*>(lut + (int64_t)out.row(blk, tr) * F::ENTRIES + tpart * EPT);
 #pragma unroll
         for (int i = 0; i < EPT / 2; ++i) tv[i] = tsrc[i];
     }
@@ -163,7 +206,7 @@ __device__ __forceinline__ void gemv_mfma_body(
     // piece j of row 2 w + h.  Chunk c goes to register slot c % CSLOTS, then
     // to the code buffer.
     const int crow = 2 * wave + (lane >> 5), cpiece = lane & 31;
-    const uint8_t* prow = packed + (int64_t)min(n0 + crow, rows - 1) * ld + (int64_t)CHB * c0 + PB * cpiece;
+    const uint8_t* prow = packed + (int64_t)out.row(blk, crow) * ld + (int64_t)CHB * c0 + PB * cpiece;
     uint32_t cr[CSLOTS][ND];
     auto load_codes = [&](int cs, int c) {
         const int cc = min(c, n - 1);
@@ -188,7 +231,7 @@ __device__ __forceinline__ void gemv_mfma_body(
 #pragma unroll
     for (int u = 0; u < XPT; ++u) {
         const int pc = min(tid + 64 * NW * u, 64 * batch - 1);
-        xsrc[u] = x + (int64_t)(pc >> 6) * cols + (int64_t)CH * c0 + 8 * (pc & 63);
+        xsrc[u] = x + (int64_t)(pc >> 6) * ld_x + (int64_t)CH * c0 + 8 * (pc & 63);
         xdst[u] = tpos((uint32_t)(pc >> 6), (uint32_t)(pc & 63));
     }
     u32x4 xw[2][XPT];
@@ -300,22 +343,13 @@ __device__ __forceinline__ void gemv_mfma_body(
     // D layout of a 16x16 block: lane l, item i -> row 4 (l / 16) + i, column l % 16.
     *(ldsf4*)(RED + 16 * (64 * wave + lane)) = acc;
     __syncthreads();
-    if (tid < RB * 16) {
-        const int row = tid >> 4, col = tid & 15;  // output row n0 + row, batch row col
-        const int l = 16 * (row >> 2) + col, i = row & 3;
+    out.done(blk, batch, part ? part + (int64_t)ks * batch * rows : nullptr, [&](int row) {
+        const int l = 16 * (row >> 2) + (tid & 15), i = row & 3;  // the lane and item of output row `row`
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) v += *(ldsf*)(RED + 16 * (64 * w + l) + 4 * i);
-        const int nr = n0 + row;
-        if (nr < rows && col < batch) {
-            if (part)
-                part[((int64_t)ks * batch + col) * rows + nr] = v;
-            else if (y_f32)
-                reinterpret_cast<float*>(y)[(int64_t)col * rows + nr] = v;
-            else
-                reinterpret_cast<uint16_t*>(y)[(int64_t)col * rows + nr] = f32_to_bf16(v);
-        }
-    }
+        return v;
+    });
 }
 
 #define GEMV_MFMA_ARGS                                                                                     \
@@ -325,14 +359,42 @@ __device__ __forceinline__ void gemv_mfma_body(
 
 template <int XROWS>
 __global__ __launch_bounds__(64 * NW) void lut6_gemv_mfma_kernel(GEMV_MFMA_ARGS) {
-    gemv_mfma_body<6, XROWS>(packed, ld, lut, x, y, y_f32, part, rows, cols, batch, nblocks, cps);
+    gemv_mfma_body<6, XROWS>(packed, ld, lut, x, cols, PlainBlock{y, y_f32, rows}, part, rows, cols, batch, nblocks, cps);
 }
 
 template <int XROWS>
 __global__ __launch_bounds__(64 * NW) void lut4_gemv_mfma_kernel(GEMV_MFMA_ARGS) {
-    gemv_mfma_body<4, XROWS>(packed, ld, lut, x, y, y_f32, part, rows, cols, batch, nblocks, cps);
+    gemv_mfma_body<4, XROWS>(packed, ld, lut, x, cols, PlainBlock{y, y_f32, rows}, part, rows, cols, batch, nblocks, cps);
 }
 #undef GEMV_MFMA_ARGS
+
+template <int BITS>
+__global__ __launch_bounds__(64 * NW) void lut_linear_mfma_kernel(const LinearBlock out, float* __restrict__ part, int nblocks,
+                                                                  int cps) {
+    const Linear& p = out.p;
+    gemv_mfma_body<BITS, 8>(p.packed, p.ld, p.lut, p.a.X, p.a.ld_x, out, part, p.N, p.K, (int)p.a.M, nblocks, cps);
+}
+
+// fqm_linear's Y from the parts [nsplit][M][N], added in order.  4 outputs a thread.
+template <bool GATED>
+__global__ __launch_bounds__(256) void lut_linear_split_sum(const Linear p, const float* __restrict__ part, int per_row, int nsplit) {
+    const int m = blockIdx.x / per_row, c = 4 * ((blockIdx.x - m * per_row) * 256 + threadIdx.x), n = min(4, p.n - c);
+    if (n <= 0) return;
+    const int64_t all = p.a.M * p.N;
+    const float* q = part + (int64_t)m * p.N + c;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < nsplit; ++s) {
+        float x[4], y[4];
+        load_values<4>(q, FQM_F32, s * all, n, x);
+        if (GATED) load_values<4>(q, FQM_F32, s * all + p.n, n, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += x[i];
+            if (GATED) w[i] += y[i];
+        }
+    }
+    finish<GATED, 4>(p, m, c, v, w, n);
+}
 
 // y[b][r] = sum over splits s (in order) of part[s][b][r]
 __global__ __launch_bounds__(256) void lut6_gemv_split_sum(const float* __restrict__ part, void* __restrict__ y,
@@ -374,6 +436,40 @@ size_t lut_gemv_mfma_workspace(const fqm_weights& w, int batch) {
     int ns, cps;
     lut_mfma_split(w, &nb, &ns, &cps);
     return ns > 1 ? (size_t)ns * (size_t)batch * (size_t)w.rows * sizeof(float) : 0;
+}
+
+// The K split of fqm_linear's workgroups, 16 rows of W each (8 of both stacked matrices).
+static void linear_mfma_split(const Linear& p, int64_t* nblocks, int* nsplit, int* cps) {
+    fqm_weights w = {};
+    w.cols = p.K;
+    w.rows = p.a.gated ? 2 * ((p.n + RB / 2 - 1) / (RB / 2) * (RB / 2)) : p.N;  // in whole blocks of both
+    lut_mfma_split(w, nblocks, nsplit, cps);
+}
+
+size_t lut_linear_mfma_workspace(const Linear& p) {
+    int64_t nb;
+    int ns, cps;
+    linear_mfma_split(p, &nb, &ns, &cps);
+    return ns > 1 ? (size_t)ns * (size_t)p.a.M * (size_t)p.N * sizeof(float) : 0;
+}
+
+hipError_t launch_lut_linear_mfma(const Linear& p, bool six, float* ws, hipStream_t s) {
+    if (p.a.M > 8) return hipErrorInvalidValue;
+    int64_t nb;
+    int ns, cps;
+    linear_mfma_split(p, &nb, &ns, &cps);
+    if (nb * ns > 0x7fffffff || (ns > 1 && !ws)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(nb * ns)), block(64 * NW);
+    float* part = ns > 1 ? ws : nullptr;
+    if (six) hipLaunchKernelGGL(lut_linear_mfma_kernel<6>, grid, block, 0, s, LinearBlock{p}, part, (int)nb, cps);
+    else hipLaunchKernelGGL(lut_linear_mfma_kernel<4>, grid, block, 0, s, LinearBlock{p}, part, (int)nb, cps);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || ns == 1) return e;
+    const int per_row = (p.n + 1023) / 1024;
+    const dim3 sums((unsigned)(p.a.M * per_row));
+    if (p.a.gated) hipLaunchKernelGGL(lut_linear_split_sum<true>, sums, dim3(256), 0, s, p, part, per_row, ns);
+    else hipLaunchKernelGGL(lut_linear_split_sum<false>, sums, dim3(256), 0, s, p, part, per_row, ns);
+    return hipGetLastError();
 }
 
 hipError_t launch_lut_gemv_mfma(const fqm_weights& w, const uint16_t* x, void* y, int y_f32, int batch,
