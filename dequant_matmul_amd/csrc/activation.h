@@ -18,7 +18,7 @@ __device__ __forceinline__ float exp_fast(float x) {
 // 1 / (1 + exp(-x)) to 4 ulp
 __device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.f + exp_fast(-x)); }
 
-__device__ __forceinline__ float activate(int act, float v) {
+__device__ __forceinline__ float activate_one(int act, float v) {
     switch (act) {
         case FQM_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
         case FQM_ACT_SILU: return v * logistic(v);
@@ -30,6 +30,22 @@ __device__ __forceinline__ float activate(int act, float v) {
         case FQM_ACT_TANH: return tanhf(v);
         default: return v;
     }
+}
+template <int ACT, int V>
+__device__ __forceinline__ void activate_as(float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = activate_one(ACT, v[i]);
+}
+// V values by one branch: what runs of it is short and lies together.
+template <int V>
+__device__ __forceinline__ void activate(int act, float (&v)[V]) {
+    if (act == FQM_ACT_NONE) return;
+    if (act == FQM_ACT_SILU) activate_as<FQM_ACT_SILU>(v);
+    else if (act == FQM_ACT_RELU) activate_as<FQM_ACT_RELU>(v);
+    else if (act == FQM_ACT_GELU) activate_as<FQM_ACT_GELU>(v);
+    else if (act == FQM_ACT_GELU_TANH) activate_as<FQM_ACT_GELU_TANH>(v);
+    else if (act == FQM_ACT_SIGMOID) activate_as<FQM_ACT_SIGMOID>(v);
+    else if (act == FQM_ACT_TANH) activate_as<FQM_ACT_TANH>(v);
 }
 
 }  // namespace

@@ -114,8 +114,9 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(const fqm_block
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) f[i] = one;
             }
+            activate<kVec>(a.gate_act, f);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) h[v][i] *= activate(a.gate_act, f[i]);
+            for (int i = 0; i < kVec; ++i) h[v][i] *= f[i];
         }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) f[i] = 0.f;

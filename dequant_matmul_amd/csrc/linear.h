@@ -107,9 +107,13 @@ __device__ __forceinline__ void finish(const Linear& p, int64_t m, int c, float 
         load_values<V>(a.bias, a.bias_dtype, c, n, b);
         if (GATED) load_values<V>(a.bias, a.bias_dtype, p.n + c, n, wb);
     }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b[i];
+    }
+    activate<V>(a.act, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        v[i] = activate(a.act, a.bias ? v[i] + b[i] : v[i]);
         if (GATED) v[i] *= a.bias ? w[i] + wb[i] : w[i];
         if (a.residual) v[i] += r[i];
     }

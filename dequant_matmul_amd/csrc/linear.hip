@@ -16,27 +16,83 @@ namespace {
 
 typedef __attribute__((address_space(3))) float lds_f;
 
-// A wave's 32 x 32 block of sums, as the matrix instruction leaves it (lane l, item r: row
-// (r % 4) + 8 (r / 4) + 4 (l / 32), column l % 32), through 1 KB of LDS of its own to neighbouring
-// outputs on a lane: 8 rows at a time, items 4 q .. 4 q + 3.  m, c: Y's row and column of the block's
-// first; rows: how many of its rows there are.
-template <bool GATED>
-__device__ __forceinline__ void finish_block(const Linear& p, lds8* own, const f32x16& acc, int64_t m, int c, int rows) {
-    constexpr int V = GATED ? 2 : 4;  // outputs of a lane
-    const int lane = threadIdx.x & 63, j = lane & 31, g = lane >> 5;
-    lds_f* put = (lds_f*)own + 128 * g + j;
-    const int row = lane >> 3, o = V * (lane & 7);
-    const lds_f* get = (lds_f*)own + 32 * row + o;
+// The epilogue of V neighbouring columns c .. of many rows, what belongs to the columns loaded once.
+template <bool GATED, int V>
+struct Columns {
+    const fqm_epilogue& a;
+    int c, n;  // n of the columns are there
+    float b[V], wb[V];
+    __device__ __forceinline__ Columns(const Linear& p, int first) : a(p.a), c(first), n(max(0, min(V, p.n - first))) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+        for (int i = 0; i < V; ++i) b[i] = wb[i] = 0.f;
+        if (a.bias && n > 0) {
+            load_values<V>(a.bias, a.bias_dtype, c, n, b);
+            if (GATED) load_values<V>(a.bias, a.bias_dtype, p.n + c, n, wb);
+        }
+    }
+    __device__ __forceinline__ void row(int64_t m, float (&v)[V], float (&w)[V]) const {
+        if (n <= 0) return;
+        float r[V];
+        if (a.residual) load_values<V>(a.residual, a.res_dtype, m * a.ld_res + c, n, r);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) put[32 * r] = acc[4 * q + r];
+        for (int i = 0; i < V; ++i) {
+            v[i] += b[i];
+            if (GATED) w[i] += wb[i];
+        }
+        activate<V>(a.act, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (GATED) v[i] *= w[i];
+            if (a.residual) v[i] += r[i];
+        }
+        store_values<V>(a.Y, a.y_dtype, m * a.ld_y + c, v, n);
+    }
+};
+
+// A wave's 32 x 32 blocks of sums, as the matrix instruction leaves them (lane l, item r: row (r % 4) + 8 (r / 4) + 4
+// (l / 32), column l % 32), go through LDS of the wave's own to neighbouring outputs on a lane, 8 rows (1 KB) at a time.
+template <int R>
+__device__ __forceinline__ void put_8_rows(lds8* own, const f32x16& acc) {  // items 4 R .. 4 R + 3
+    lds_f* put = (lds_f*)own + 128 * ((threadIdx.x >> 5) & 1) + (threadIdx.x & 31);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) put[32 * r] = acc[4 * R + r];
+}
+template <bool GATED, int V>
+__device__ __forceinline__ void finish_8_rows(const Columns<GATED, V>& cols, const lds8* own, int64_t m, int rows) {
+    const int row = (threadIdx.x & 63) >> 3;
+    const lds_f* get = (const lds_f*)own + 32 * row + V * (threadIdx.x & 7);
+    float v[V], w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = get[i], w[i] = GATED ? get[16 + i] : 0.f;
+    if (row < rows) cols.row(m + row, v, w);
+}
+
+// All MB blocks of a wave, of its own 1024 KB bytes (a multiple of 1 KB) of each of two buffers: as many rows at once
+// as these hold, so that the epilogue's code is there few times (it runs once a tile: what it costs is fetching it,
+// and choosing the sums by a loop's counter cost 112 selections a block).  m, c: Y's row and the wave's first column;
+// rows: how many rows there are from m on.
+template <bool GATED, int MB, int KB>
+__device__ __forceinline__ void finish_blocks(const Linear& p, lds8* x0, lds8* x1, const f32x16 (&acc)[MB], int64_t m, int c, int rows) {
+    constexpr int V = GATED ? 2 : 4, EACH = KB >= 4 ? 4 : KB, ALL = 4 * MB, AT_ONCE = 2 * EACH < ALL ? 2 * EACH : ALL;
+    const Columns<GATED, V> cols(p, c + V * (threadIdx.x & 7));
+#pragma unroll
+    for (int r0 = 0; r0 < ALL; r0 += AT_ONCE) {
+#pragma unroll
+        for (int r = 0; r < AT_ONCE; ++r) {
+            lds8* to = (r < EACH ? x0 : x1) + 1024 * (r % EACH);
+            const f32x16& from = acc[(r0 + r) / 4];
+            switch ((r0 + r) % 4) {
+                case 0: put_8_rows<0>(to, from); break;
+                case 1: put_8_rows<1>(to, from); break;
+                case 2: put_8_rows<2>(to, from); break;
+                default: put_8_rows<3>(to, from); break;
+            }
+        }
         wave_lds_order();
-        float v[V], w[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = get[i], w[i] = GATED ? get[16 + i] : 0.f;
+#pragma unroll 1
+        for (int r = 0; r < AT_ONCE; ++r)
+            finish_8_rows(cols, (r < EACH ? x0 : x1) + 1024 * (r % EACH), m + 8 * (r0 + r), rows - 8 * (r0 + r));
         wave_lds_order();
-        if (8 * q + row < rows) finish<GATED, V>(p, m + 8 * q + row, c + o, v, w, min(V, p.n - c - o));
     }
 }
 
@@ -46,6 +102,7 @@ template <int BITS, int BM, int NW, bool GATED, bool PARTIAL>
 __global__ __launch_bounds__(64 * NW) void linear_tile_kernel(const Linear p, int mtiles, int nt0, int ksplit,
                                                               float* __restrict__ part) {
     constexpr int BN = 32 * NW, OUT = GATED ? BN / 2 : BN;
+    constexpr int OWN = BM * 128 / NW;  // of an X buffer, a wave's in the epilogue
     FQM_GEMM_TILE_LDS(BITS, BM, NW);
     const fqm_epilogue& a = p.a;
     const int b = blockIdx.x, tt = b / ksplit, ks = b - tt * ksplit;
@@ -61,10 +118,10 @@ __global__ __launch_bounds__(64 * NW) void linear_tile_kernel(const Linear p, in
                                     [&](int row, int col, float v) { part[(size_t)b * (BM * BN) + row * BN + col] = v; });
         else
             gemm_tile<BITS, BM, NW>(FQM_GEMM_TILE_LDS_ARGS, X, 0, x_off, p.packed, p.ld, p.lut, wr, t0, t1 - t0,
-                                    [&](int i, const f32x16& acc) {
+                                    [&](const f32x16(&acc)[BM / 32]) {
                                         const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-                                        finish_block<GATED>(p, (lds8*)s_x0 + 1024 * wn, acc, m0 + 32 * i, nt * OUT + OUT / NW * wn,
-                                                            rows - 32 * i);
+                                        finish_blocks<GATED, BM / 32, OWN / 1024>(p, (lds8*)s_x0 + OWN * wn, (lds8*)s_x1 + OWN * wn, acc, m0,
+                                                                                  nt * OUT + OUT / NW * wn, rows);
                                     });
     };
     if constexpr (GATED) tile(StackedRows{p.n, nt * OUT});
@@ -305,12 +362,7 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may still be writing this workgroup's LDS
         if (s0 == 0 && s1 == stages) {
             __syncthreads();
-#pragma unroll 1
-            for (int i = 0; i < MB; ++i) {
-                f32x16 sums = acc[0];
-                if (MB > 1 && i == 1) sums = acc[MB - 1];
-                finish_block<GATED>(p, XS[0] + 1024 * wave, sums, 32 * i, OUT * (NW * nt + wave), M - 32 * i);
-            }
+            finish_blocks<GATED, MB, MX>(p, XS[0] + 1024 * MX * wave, XS[1] + 1024 * MX * wave, acc, 0, OUT * (NW * nt + wave), M);
         } else {
             float* q = part + ((size_t)2 * blockIdx.x + (u != u0)) * M * BN + 32 * wave + j;
 #pragma unroll
@@ -424,43 +476,63 @@ __global__ __launch_bounds__(256) void linear_of_nothing(const Linear p, int64_t
     else finish<false, 2>(p, m, c, v, w, 1);
 }
 
-// Tiles and what is split.  Up to 256 rows all tiles are split alike, so that the
-// grid has enough workgroups; above, whole rounds of 256-row tiles (one per compute
-// unit) run as one launch and the N tiles that are left for a partial round are split
-// along K into as many parts as make that round shortest.
+// Tiles and what is split.  64- and 128-row tiles (4 waves; several a compute unit) are all split along K alike; of
+// 256-row tiles (8 waves, one a compute unit) whole rounds run as one launch, and the N tiles that are left for a
+// partial round are split into as many parts as make that round shortest.
 struct LinearPlan {
     int bm, nw, mtiles, ntiles;
     int nt_main;      // N tiles [0, nt_main) are not split
     int ksplit;       // K parts of the others
     int64_t tail;     // the others
+    double us;        // what it should take
     size_t part_bytes;
 };
 
-LinearPlan linear_plan(int64_t N, int64_t K, int64_t M, bool gated) {
+// The time is that of the compute unit with the most workgroups: its K steps (and 6 for each workgroup's start) at
+// what one takes there, more than its share where a workgroup is alone, and the parts' way through memory with a
+// second launch.
+LinearPlan tile_plan(int bm, int64_t N, int64_t K, int64_t M, bool gated) {
     LinearPlan p;
-    p.bm = M <= 32 ? 32 : M <= 256 ? 64 : 256;
-    p.nw = p.bm == 256 ? 8 : 4;
-    const int64_t per = gated ? 16 * p.nw : 32 * p.nw, n = gated ? N / 2 : N, steps = K / BK;
-    p.mtiles = (int)((M + p.bm - 1) / p.bm);
-    p.ntiles = p.nt_main = (int)((n + per - 1) / per);
-    p.ksplit = 1;
-    p.tail = 0;
+    p.bm = bm;
+    p.nw = bm == 256 ? 8 : 4;
+    const int64_t per = gated ? 16 * p.nw : 32 * p.nw, n = gated ? N / 2 : N, steps = K / BK, cus = compute_units();
+    const double step_us = bm == 64 ? 0.42 : bm == 128 ? 0.5 : 1.7, alone_us = bm == 64 ? 0.5 : bm == 128 ? 0.6 : 1.7, start = 6;
+    auto steps_us = [&](int64_t groups, int64_t of) {
+        const int64_t each = (groups + cus - 1) / cus;
+        return (each == 1 ? alone_us : each * step_us) * (of + start);
+    };
+    p.mtiles = (int)((M + bm - 1) / bm);
+    p.ntiles = (int)((n + per - 1) / per);
     const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
-    if (p.bm < 256) {
-        const int64_t parts = std::min<int64_t>({768 / tiles, steps / 8, (int64_t)8});
-        if (parts > 1) p.ksplit = (int)parts, p.nt_main = 0;
-    } else if (const int64_t slots = compute_units(); tiles % slots) {
-        const int nt_main = (int)(tiles / slots * slots / p.mtiles);
-        const int64_t tail = (int64_t)(p.ntiles - nt_main) * p.mtiles;
-        int64_t best = (tail + slots - 1) / slots * steps;
-        for (int64_t k = 2; k <= steps / 8 && tail * k * (256 * 256 * 4) <= ((int64_t)256 << 20); ++k) {
-            const int64_t len = (tail * k + slots - 1) / slots * ((steps + k - 1) / k);
-            if (len < best) best = len, p.ksplit = (int)k, p.nt_main = nt_main;
-        }
-    }
+    p.nt_main = bm == 256 ? (int)(tiles / cus * cus / p.mtiles) : 0;
     p.tail = (int64_t)(p.ntiles - p.nt_main) * p.mtiles;
-    p.part_bytes = (size_t)p.tail * p.ksplit * p.bm * 32 * p.nw * 4;
+    p.us = 1e30;
+    const double tile_bytes = 4.0 * bm * 32 * p.nw;
+    for (int64_t k = 1; k <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, bm == 256 ? steps / 8 : 8)); ++k) {
+        const double parts = k == 1 ? 0 : 2 * k * p.tail * tile_bytes;
+        if (k > 1 && parts > 2 * (256 << 20)) break;
+        const double us = p.tail == 0 ? 0 : steps_us(p.tail * k, (steps + k - 1) / k) + (k > 1 ? 3 + parts / 8e6 : 0);
+        if (us < p.us) p.us = us, p.ksplit = (int)k;
+    }
+    if (tiles > p.tail) p.us += steps_us(tiles - p.tail, steps);
+    if (p.ksplit == 1) p.nt_main = p.ntiles, p.tail = 0;
+    p.part_bytes = p.ksplit > 1 ? (size_t)(p.tail * p.ksplit * tile_bytes) : 0;
     return p;
+}
+
+// The height whose time should be the least.  Measured on one MI355X, us with 64 / 128 / 256 rows: 6-bit 5120 -> 17408
+// at 64 rows 37 / - / -, 96 rows 66 / 48 / 77, 128 rows 68 / 50 / 79, 192 rows 76 / 85 / 84, 256 rows 107 / 88 / 90,
+// 320 rows 113 / 99 / 139, 512 rows 168 / 148 / 152; 6-bit 5120 -> 34816 at 512 rows 304 / 238 / 197; 6-bit 17408 ->
+// 5120 at 128 rows 53 / 53 / 80, 256 rows 88 / 71 / 90, 512 rows 168 / 121 / 192; 4-bit 4160 -> 1000 at 96 rows 13.0 /
+// 14.0 / 22, 512 rows 22 / 21 / 27.
+LinearPlan linear_plan(int64_t N, int64_t K, int64_t M, bool gated) {
+    LinearPlan best = tile_plan(64, N, K, M, gated);
+    for (const int bm : {128, 256}) {
+        if (M <= bm / 2) break;
+        const LinearPlan p = tile_plan(bm, N, K, M, gated);
+        if (p.us < best.us) best = p;
+    }
+    return best;
 }
 
 template <int BITS, int BM, int NW, bool GATED>
@@ -488,8 +560,8 @@ template <int BITS, bool GATED>
 hipError_t launch_tile_bits(const Linear& p, void* ws, hipStream_t s) {
     float* part = static_cast<float*>(ws);
     const LinearPlan plan = linear_plan(p.N, p.K, p.a.M, GATED);
-    if (plan.bm == 32) return launch_tiles<BITS, 32, 4, GATED>(p, plan, part, s);
     if (plan.bm == 64) return launch_tiles<BITS, 64, 4, GATED>(p, plan, part, s);
+    if (plan.bm == 128) return launch_tiles<BITS, 128, 4, GATED>(p, plan, part, s);
     return launch_tiles<BITS, 256, 8, GATED>(p, plan, part, s);
 }
 

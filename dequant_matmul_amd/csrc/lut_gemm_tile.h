@@ -118,9 +118,9 @@ struct RunOfRows {
 // of tile row `row` of X below X + xtile (32 bits in all; callers keep X below
 // 2 GiB from X on, and rows past the end at some valid row); out(row, col, v)
 // takes the fp32 sum of tile row `row` and tile column `col`, every one of
-// them, in a fixed order; an `out` of (block, sums) takes a wave's 32 x 32 blocks
-// of sums whole, as the matrix instruction leaves them, behind a barrier after which
-// no wave touches the LDS any more.  Where before is not NoPrep, before(scratch) runs ahead of
+// them, in a fixed order; an `out` of (sums) takes a wave's 32 x 32 blocks of sums
+// as the matrix instruction leaves them, behind a barrier after which the tile
+// touches the LDS no more.  Where before is not NoPrep, before(scratch) runs ahead of
 // the first out between two barriers, with at least 4 KB of LDS.
 // tab, x0, x1, x2: LDS objects of their own (FQM_GEMM_TILE_LDS), so that the
 // compiler sees that the table gathers do not wait for the direct loads of X.
@@ -339,17 +339,9 @@ __device__ __forceinline__ void gemm_tile(lds8* tab, lds8* x0, lds8* x1, lds8* x
         __syncthreads();
     }
     // D layout of a 32x32 block: lane l, item r -> row (r % 4) + 8 * (r / 4) + 4 * (l / 32), column l % 32.
-    if constexpr (std::is_invocable<Out, int, const f32x16&>::value) {
+    if constexpr (std::is_invocable<Out, const f32x16(&)[MB]>::value) {
         __syncthreads();
-        // one copy of `out`, whose code may be long: eight of them left the sums in scratch memory
-#pragma unroll 1
-        for (int i = 0; i < MB; ++i) {
-            f32x16 sums = acc[0];
-#pragma unroll
-            for (int b = 1; b < MB; ++b)
-                if (i == b) sums = acc[b];
-            out(i, sums);
-        }
+        out(acc);
     } else {
 #pragma unroll
         for (int i = 0; i < MB; ++i)
