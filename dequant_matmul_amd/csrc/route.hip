@@ -2,174 +2,440 @@
 // the plan of the products grouped by expert (a stable counting sort of the
 // T k slots by expert).
 //
-// Choice.  c = score + bias in fp64 (without a bias the logits themselves, whose
-// order is the scores'), the groups of best score, then k times the largest
-// that is left; ties to the lowest index.  One wave per token, expert e on
-// lane e mod 64.
+// Choice: one wave per token, expert e on lane e mod 64.  An expert's score + bias (its logit, without
+// a bias) in fp32, as an integer of the same order, is a key; a choice is a maximum over the wave (six DPP
+// instructions) and, of the lanes that have it, the lowest expert.  Two more than k are chosen.  Where
+// fp32's errors leave the order of the first k + 1 open (one token in some hundreds), the chosen ones' scores
+// are formed again in fp64, a lane each, and ranked; where they leave open even which these are, all
+// experts' are.
 //
-// Plan.  Tiles of kTileSlots slots count their experts; each tile then adds up
-// the counts of the tiles in front of it and ranks its slots, wave by wave:
-// lanes with the same expert find each other with one ballot per bit of its
-// number.  No counter is taken by whoever comes first, so the order of a
-// group's rows is the slots' order, whatever the timing.
+// Plan: up to kTiles tiles of tokens count their experts as they choose; a second launch
+// adds up the counts of the tiles in front of each, and ranks its slots wave by wave: lanes
+// with the same expert find each other with one ballot per bit of its number.  No
+// counter is taken by whoever comes first, so the order of a group's rows is the slots'
+// order, whatever the timing.  Few tokens are one workgroup's work, in one launch.
 #include <algorithm>
 
+#include "activation.h"
 #include "fqm_layer.h"
 
 namespace fqm {
 namespace {
 
-constexpr int kWaves = 4;          // of the choice: a token each
 constexpr int kMaxE = 1024;
-constexpr int kPlanWaves = 8;
-constexpr int kTileSlots = 2048;   // of the plan, per workgroup
+constexpr int kFewWaves = 4;         // of a choosing workgroup with a short tile
+constexpr int kTiles = 256;          // at most so many tiles
+constexpr int kPlaceWaves = 8;
+constexpr int kSmallTokens = 8;      // one workgroup's work
 constexpr float kLargest = 3.4028234663852886e38f;
 
 __device__ __forceinline__ float logit(const fqm_routing& a, int64_t at) {
     const float l = a.x_dtype == FQM_F32 ? static_cast<const float*>(a.logits)[at]
                                          : bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at]);
-    return fminf(l, kLargest) == l || l != l ? l : kLargest;
+    return l > kLargest ? kLargest : l;  // a NaN stays one
+}
+// The sum over the wave in fp64, the same in every lane.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROW_MASK, 0xF, false);
+    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    v = dpp_add_f64<0xB1, 0xF>(v);
+    v = dpp_add_f64<0x4E, 0xF>(v);
+    v = dpp_add_f64<0x141, 0xF>(v);
+    v = dpp_add_f64<0x140, 0xF>(v);
+    v = dpp_add_f64<0x142, 0xA>(v);
+    v = dpp_add_f64<0x143, 0xC>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// The largest value of the wave and the lowest index that has it.
+// The largest of the wave's values (0 where it has none), the same in every lane.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROW_MASK, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = dpp_max<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+    v = dpp_max<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+    v = dpp_max<0x141, 0xF>(v);  // row_half_mirror
+    v = dpp_max<0x140, 0xF>(v);  // row_mirror
+    v = dpp_max<0x142, 0xA>(v);  // row_bcast:15
+    v = dpp_max<0x143, 0xC>(v);  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Floats in the order of unsigned integers, and back.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ float wave_max_f(float v) { return from_ordered(wave_max(ordered(v))); }
+
+__device__ __forceinline__ float wave_total(float v) {  // the sum, the same in every lane
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_lane63(v)), 63));
+}
+__device__ __forceinline__ float at_lane(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ double at_lane(double v, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, l), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// A wave's token: its logits, its experts' biases, and which of them are open (bit v: expert lane + 64 v).
+template <int NV>
+struct Token {
+    float l[NV], b[NV];
+    uint32_t open;
+};
+// What lane j < k has chosen: its expert (-1: none) and its logit.
+struct Chosen {
+    int expert;
+    float l;
+};
+
+// One step of joining the best and second best of neighbouring lanes.
 template <class V>
-__device__ __forceinline__ void wave_best(V& v, int& i) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        const V ov = __shfl_xor(v, o, 64);
-        const int oi = __shfl_xor(i, o, 64);
-        if (ov > v || (ov == v && oi < i)) v = ov, i = oi;
-    }
+__device__ __forceinline__ void join(V& best, V& second, V ob, V os) {
+    const V low = ob < best ? ob : best;
+    best = ob > best ? ob : best;
+    second = os > second ? os : second;
+    second = low > second ? low : second;
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Scores of a lane's NV logits (in fp64) under the call's rule; open: bit v is
-// set where expert lane + 64 v is open.
-template <int NV>
-__device__ __forceinline__ void scores_f64(const fqm_routing& a, const float (&l)[NV], uint32_t open, double (&s)[NV]) {
-    if (a.score == FQM_SIGMOID) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) s[v] = 1.0 / (1.0 + exp(-(double)l[v]));
-        return;
+// The groups that stay, as a mask, from the values c[0 .. E) in LDS (-infinity: closed): by their best value, or the
+// sum of their two best.  near: whether values that may be off by err leave it open which groups stay.
+template <class V>
+__device__ __forceinline__ uint64_t keep_groups(const fqm_routing& a, const V* c, bool two, V err, bool* near) {
+    const int lane = threadIdx.x & 63, per = a.E / a.groups;
+    const int shift = __builtin_clz(a.groups - 1) - 26;  // 2^shift lanes a group: 64 over groups, rounded up to a power of two
+    const int g = lane >> shift, at = lane & ((1 << shift) - 1);
+    V best = -INFINITY, second = -INFINITY;
+    if (g < a.groups)
+        for (int i = at; i < per; i += 1 << shift) {
+            const V x = c[g * per + i];
+            if (x > best) second = best, best = x;
+            else if (x > second) second = x;
+        }
+    if (shift >= 1) join(best, second, dpp_move<0xB1>(best), dpp_move<0xB1>(second));    // quad_perm [1,0,3,2]
+    if (shift >= 2) join(best, second, dpp_move<0x4E>(best), dpp_move<0x4E>(second));    // quad_perm [2,3,0,1]
+    if (shift >= 3) join(best, second, dpp_move<0x141>(best), dpp_move<0x141>(second));  // row_half_mirror
+    if (shift >= 4) join(best, second, dpp_move<0x140>(best), dpp_move<0x140>(second));  // row_mirror
+    if (shift >= 5) join(best, second, __shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
+    if (two && second > -INFINITY) best += second;
+    // each group against the others, in every lane of the group
+    int before = 0;
+    for (int o = 0; o < a.groups; ++o) {
+        const V x = at_lane(best, o << shift);
+        before += x > best || (x == best && o < g);
     }
-    float m = -kLargest;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-        if (open >> v & 1) m = fmaxf(m, l[v]);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    double z = 0.0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        s[v] = open >> v & 1 ? exp((double)l[v] - (double)m) : 0.0;
-        z += s[v];
+    const uint64_t first_lanes = __ballot(at == 0 && g < a.groups);
+    uint64_t stay = __ballot(before < a.top_groups) & first_lanes, kept = 0;
+    if (err > 0 && a.top_groups < a.groups) {
+        // the last that stays against the first that does not (one without an open expert stays last)
+        const V x = at_lane(best, __builtin_ctzll(__ballot(before == a.top_groups - 1) & first_lanes));
+        const V y = at_lane(best, __builtin_ctzll(__ballot(before == a.top_groups) & first_lanes));
+        *near = !(x - y > 2 * err) && !(y == -INFINITY);
     }
-    z = wave_sum_f64(z);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) s[v] = z > 0.0 ? s[v] / z : 0.0;
+    for (; stay; stay &= stay - 1) kept |= 1ull << (__builtin_ctzll(stay) >> shift);
+    return kept;
 }
 
-template <int NV>
-__global__ __launch_bounds__(64 * kWaves) void route_choose(const fqm_routing a) {
-    __shared__ double s_c[kWaves][64 * NV];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-    if (t >= a.T) return;
+// The choice with scores in fp64, for the few tokens that need it: from memory again, in loops, so that it takes no
+// registers from the others.  s_c: E values of LDS of the wave's own.
+__device__ __forceinline__ Chosen choose_exactly(const fqm_routing& a, int64_t row, double* s_c) {
+    const int lane = threadIdx.x & 63;
     const double kClosed = -INFINITY;
-    float l[NV];
-    double c[NV], s[NV];
-    uint32_t open = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = lane + 64 * v;
-        l[v] = -INFINITY;
-        if (e < a.E) {
-            l[v] = logit(a, t * a.ld_x + e);
-            const float b = a.bias ? a.bias[e] : 0.f;
-            if (l[v] > -INFINITY && b > -INFINITY) open |= 1u << v;
-        }
+    auto value = [&](int e) { return logit(a, row * a.ld_x + e); };
+    auto bias = [&](int e) { return a.bias ? a.bias[e] : 0.f; };
+    auto open = [&](int e) { return value(e) > -INFINITY && bias(e) > -INFINITY; };
+    double m = -(double)kLargest, z = 0.0;
+    if (a.score == FQM_SOFTMAX) {
+        float top = -kLargest;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 64)
+            if (open(e)) top = fmaxf(top, value(e));
+        m = wave_max_f(top);
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 64)
+            if (open(e)) z += exp((double)value(e) - m);
+        z = wave_sum_f64(z);
     }
+    auto score = [&](int e) {
+        const double l = value(e);
+        return a.score == FQM_SOFTMAX ? exp(l - m) / z : 1.0 / (1.0 + exp(-l));
+    };
     const bool sums = a.groups > 1 && a.group_score == FQM_GROUP_TOP2;
-    scores_f64<NV>(a, l, open, s);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = lane + 64 * v;
-        const double sb = a.bias && e < a.E ? s[v] + (double)a.bias[e] : s[v];
-        c[v] = open >> v & 1 ? (a.bias ? sb : (double)l[v]) : kClosed;
-        if (a.groups > 1 && e < a.E) s_c[wave][e] = open >> v & 1 ? (sums ? sb : c[v]) : kClosed;
-    }
-    if (a.groups > 1) {
+    uint64_t kept = ~0ull;
+    const int per = a.E / a.groups;
+    for (int pass = a.groups > 1 ? 0 : 1; pass < 2; ++pass) {  // the groups' values, then the experts'
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 64) {
+            double c = kClosed;
+            if (open(e) && (pass == 0 || kept >> (e / per & 63) & 1))
+                c = a.bias || (pass == 0 && sums) ? score(e) + (double)bias(e) : (double)value(e);
+            s_c[e] = c;
+        }
         wave_lds_order();
-        const int per = a.E / a.groups;
-        // lane g < groups: its group's score, and how many groups come before it
-        double best = kClosed, second = kClosed;
-        if (lane < a.groups)
-            for (int i = 0; i < per; ++i) {
-                const double x = s_c[wave][lane * per + i];
-                if (x > best) second = best, best = x;
-                else if (x > second) second = x;
-            }
-        if (sums && second > kClosed) best += second;
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const double o = __shfl(best, g, 64);
-            before += o > best || (o == best && g < lane);
-        }
-        const uint64_t kept = __ballot(lane < a.groups && before < a.top_groups);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int e = lane + 64 * v;
-            if (e < a.E && !(kept >> (e / per) & 1)) c[v] = kClosed;
+        if (pass == 0) {
+            bool near;
+            kept = keep_groups<double>(a, s_c, sums, 0.0, &near);
+            wave_lds_order();
         }
     }
-    // lane j keeps the j-th choice
-    int mine = -1;
-    float ml = 0.f;
-    double ms = 0.0;
+    Chosen mine = {-1, 0.f};
     for (int j = 0; j < a.k; ++j) {
         double bv = kClosed;
         int be = kMaxE;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 64)
+            if (s_c[e] > bv) bv = s_c[e], be = e;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (c[v] > bv) bv = c[v], be = lane + 64 * v;
-        wave_best(bv, be);
+        for (int o = 32; o >= 1; o >>= 1) {
+            const double ov = __shfl_xor(bv, o, 64);
+            const int oi = __shfl_xor(be, o, 64);
+            if (ov > bv || (ov == bv && oi < be)) bv = ov, be = oi;
+        }
         if (!(bv > kClosed)) break;  // uniform
-        float bl = 0.f;
-        double bs = 0.0;
+        if (lane == (be & 63)) s_c[be] = kClosed;
+        wave_lds_order();
+        if (lane == j) mine = {be, value(be)};
+    }
+    return mine;
+}
+
+// LDS of a wave: two fp32 values an expert, or one in fp64.
+template <int NV>
+union WaveLds {
+    float f[2][64 * NV];
+    double d[64 * NV];
+};
+
+// A token's expert and weight in lane j < k.
+template <int NV>
+__device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const Token<NV>& t, WaveLds<NV>* lds, int* expert,
+                                       float* weight) {
+    const int lane = threadIdx.x & 63;
+    const bool sums = a.groups > 1 && a.group_score == FQM_GROUP_TOP2, softmax = a.score == FQM_SOFTMAX;
+    const bool scored = a.bias || sums || (softmax && !a.renormalise);  // whether all scores are needed
+    float s[NV], c[NV], top = 0.f;
+    double z = 1.0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) s[v] = 0.f;
+    if (scored && softmax) {
+        top = -kLargest;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (be == lane + 64 * v) c[v] = kClosed, bl = l[v], bs = s[v];
-        bl = __shfl(bl, be & 63, 64);
-        bs = __shfl(bs, be & 63, 64);
-        if (lane == j) mine = be, ml = bl, ms = bs;
+            if (t.open >> v & 1) top = fmaxf(top, t.l[v]);
+        top = wave_max_f(top);
+        float part = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            s[v] = t.open >> v & 1 ? exp_fast(t.l[v] - top) : 0.f;
+            part += s[v];
+        }
+        z = wave_sum_f64((double)part);
+        const float r = z > 0.0 ? 1.f / (float)z : 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) s[v] *= r;
+    } else if (scored) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) s[v] = logistic(t.l[v]);
     }
-    float w = (float)ms;
+    // How far s + bias may be off, U = 2^-24: 7 U of a sigmoid and U of the sum; of a softmax 4 U for the exponential, U
+    // for its argument, 16 U and what the exponentials have for z, 3 U for the product.
+    const float unit = softmax ? 0x1p-18f : 0x1p-20f;
+    float bmax = 0.f;
+    if (a.bias) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (t.open >> v & 1) bmax = fmaxf(bmax, fabsf(t.b[v]));
+        bmax = wave_max_f(bmax);
+    }
+    uint32_t key[NV];  // 0: closed
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        c[v] = a.bias ? s[v] + t.b[v] : t.l[v];
+        key[v] = t.open >> v & 1 ? ordered(c[v]) : 0u;
+    }
+    bool near = false;
+    if (a.groups > 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int e = lane + 64 * v;
+            if (e < a.E) lds->f[0][e] = t.open >> v & 1 ? (sums && !a.bias ? s[v] : c[v]) : -INFINITY;
+        }
+        wave_lds_order();
+        const float off = unit * (1.f + bmax);
+        const uint64_t kept = keep_groups<float>(a, lds->f[0], sums, sums ? 2 * off : a.bias ? off : 0.f, &near);
+        wave_lds_order();
+        const int per = a.E / a.groups;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int e = lane + 64 * v;
+            if (e < a.E && !(kept >> (e / per) & 1)) key[v] = 0u;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        lds->f[0][lane + 64 * v] = t.l[v];
+        lds->f[1][lane + 64 * v] = c[v];
+    }
+    // the k + 2 first, the j-th in lane j
+    Chosen got = {-1, 0.f};
+    int found = 0;
+    for (; found < a.k + 2; ++found) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int v = 1; v < NV; ++v) m = max(m, key[v]);
+        m = wave_max(m);
+        if (m == 0u) break;  // uniform
+        int e = kMaxE;
+#pragma unroll
+        for (int v = NV - 1; v >= 0; --v) {
+            const uint64_t at = __ballot(key[v] == m);
+            if (at) e = 64 * v + __builtin_ctzll(at);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (lane + 64 * v == e) key[v] = 0u;
+        if (lane == found) got.expert = e;
+    }
+    wave_lds_order();
+    float cj = 0.f;
+    if (got.expert >= 0) {
+        got.l = lds->f[0][got.expert];
+        cj = lds->f[1][got.expert];
+    }
+    wave_lds_order();
+    if (a.bias && !near) {  // without a bias the keys are the logits
+        const float err = unit * (fabsf(at_lane(cj, 0)) + 2 * bmax);  // no score is larger than the first c and bmax
+        const float cn = __shfl(cj, min(lane + 1, 63), 64);
+        const bool unsure = lane < min(a.k, found - 1) && !(cj - cn > 2 * err);
+        if (__ballot(unsure)) {
+            if (softmax) {
+                z = 0.0;
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    if (t.open >> v & 1) z += exp((double)t.l[v] - (double)top);
+                z = wave_sum_f64(z);
+            }
+            double exact = -INFINITY;
+            if (lane < found) {
+                const double l = got.l;
+                exact = (softmax ? exp(l - (double)top) / z : 1.0 / (1.0 + exp(-l))) + (double)a.bias[got.expert];
+            }
+            int rank = 0;
+            for (int o = 0; o < found; ++o) {
+                const double x = at_lane(exact, o);
+                const int e = __builtin_amdgcn_readlane(got.expert, o);
+                rank += x > exact || (x == exact && e < got.expert);
+            }
+            // what was not found is at most the last one's c and two errors: the k-th has to be above it
+            if (found == a.k + 2) {
+                const double kth = at_lane(exact, __builtin_ctzll(__ballot(lane < found && rank == a.k - 1)));
+                near = !(kth > (double)at_lane(cj, found - 1) + 2 * (double)err);
+            }
+            if (lane < found) {
+                lds->f[0][rank] = __int_as_float(got.expert);
+                lds->f[1][rank] = got.l;
+            }
+            wave_lds_order();
+            if (lane < found) {
+                got.expert = __float_as_int(lds->f[0][lane]);
+                got.l = lds->f[1][lane];
+            }
+            wave_lds_order();
+        }
+    }
+    if (near) got = choose_exactly(a, row, lds->d);
+
+    const bool live = got.expert >= 0 && lane < a.k;  // lanes k and k + 1 have the first that are not chosen
+    float w;
     if (a.renormalise) {
         // scores up to a common factor that keeps the largest away from zero: exp(l), or
         // exp(min(l, 0)) / (1 + exp(-|l|))
-        const float e = a.score == FQM_SOFTMAX ? ml : fminf(ml, 0.f);
-        float m = mine >= 0 ? e : -INFINITY;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        w = mine >= 0 ? expf(e - m) : 0.f;
-        if (a.score == FQM_SIGMOID) w /= 1.f + expf(-fabsf(ml));
-        const float sum = wave_sum(w);
+        const float e = softmax ? got.l : fminf(got.l, 0.f);
+        const float m = wave_max_f(live ? e : -INFINITY);
+        w = live ? expf(e - m) : 0.f;
+        if (!softmax) w /= 1.f + expf(-fabsf(got.l));
+        const float sum = wave_total(w);
         w = sum > 0.f ? w / sum : 0.f;
+    } else {
+        w = softmax ? (float)(exp((double)got.l - (double)top) / z) : 1.f / (1.f + expf(-got.l));
     }
-    if (lane < a.k) {
-        a.expert[t * a.k + lane] = mine;
-        a.weight[t * a.k + lane] = mine >= 0 ? w * a.scale : 0.f;
+    *expert = got.expert;
+    *weight = live ? w * a.scale : 0.f;
+}
+
+template <int NV>
+__device__ __forceinline__ void load_token(const fqm_routing& a, int64_t row, const float (&b)[NV], uint32_t there, Token<NV>* t) {
+    const int lane = threadIdx.x & 63;
+    t->open = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int e = lane + 64 * v;
+        t->l[v] = e < a.E ? logit(a, row * a.ld_x + e) : -INFINITY;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        t->b[v] = b[v];
+        if ((there >> v & 1) && t->l[v] > -INFINITY) t->open |= 1u << v;
+    }
+}
+// The bias of a lane's experts; bit v of the answer: expert lane + 64 v may be chosen.
+template <int NV>
+__device__ __forceinline__ uint32_t load_bias(const fqm_routing& a, float (&b)[NV]) {
+    const int lane = threadIdx.x & 63;
+    uint32_t there = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int e = lane + 64 * v;
+        b[v] = a.bias && e < a.E ? a.bias[e] : 0.f;
+        if (e < a.E && b[v] > -INFINITY) there |= 1u << v;
+    }
+    return there;
+}
+
+// Chooses for the tokens first + wave, first + wave + NW, ... below end; the next one's logits are on their way meanwhile.
+// done(t, expert, weight): lane j < k has token t's j-th.
+template <int NV, int NW, class Done>
+__device__ __forceinline__ void choose_all(const fqm_routing& a, int64_t first, int64_t end, WaveLds<NV>* lds, Done done) {
+    float b[NV];
+    const uint32_t there = load_bias<NV>(a, b);
+    int64_t t = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= end) return;
+    Token<NV> token, next;
+    load_token<NV>(a, t, b, there, &token);
+    for (; t < end; t += NW, token = next) {
+        load_token<NV>(a, min(t + NW, end - 1), b, there, &next);
+        int expert;
+        float weight;
+        choose<NV>(a, t, token, lds, &expert, &weight);
+        done(t, expert, weight);
     }
 }
 
-// Slot i's place in the sort: its expert, E for none.
-__device__ __forceinline__ int slot_key(const fqm_routing& a, int64_t i) {
-    const int e = a.expert[i];
-    return e < 0 ? a.E : e;
-}
+// A slot's place in the sort: its expert, E for none.
+__device__ __forceinline__ int key_of(const fqm_routing& a, int expert) { return expert < 0 ? a.E : expert; }
 // The lanes (of those in `live`) whose key is this lane's.
 __device__ __forceinline__ uint64_t same_key(int key, uint64_t live) {
     uint64_t m = live;
@@ -180,54 +446,22 @@ __device__ __forceinline__ uint64_t same_key(int key, uint64_t live) {
     }
     return m;
 }
-
-// hist[tile][0 .. E]: how many slots of the tile go to each expert (and to none).
-__global__ __launch_bounds__(64 * kPlanWaves) void route_count(const fqm_routing a, int* __restrict__ hist, int64_t slots) {
-    __shared__ int s_n[kMaxE + 1];
-    for (int e = threadIdx.x; e <= a.E; e += 64 * kPlanWaves) s_n[e] = 0;
-    __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * kTileSlots;
-    for (int i = threadIdx.x; i < kTileSlots; i += 64 * kPlanWaves)
-        if (first + i < slots) atomicAdd(&s_n[slot_key(a, first + i)], 1);
-    __syncthreads();
-    for (int e = threadIdx.x; e <= a.E; e += 64 * kPlanWaves) hist[(int64_t)blockIdx.x * (a.E + 1) + e] = s_n[e];
+__device__ __forceinline__ int lanes_before(uint64_t m) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
-
-// The plan's rows of one tile of slots.
-__global__ __launch_bounds__(64 * kPlanWaves) void route_place(const fqm_routing a, const int* __restrict__ hist, int64_t slots) {
-    constexpr int NT = 64 * kPlanWaves, PER = kTileSlots / kPlanWaves;
-    __shared__ int s_all[kMaxE + 1];                // an expert's slots of all tiles, then its first row
-    __shared__ int s_at[kPlanWaves][kMaxE + 1];     // its next row for each wave's slots
-    __shared__ int s_sum[kPlanWaves];
+__device__ __forceinline__ void place(const fqm_routing& a, int to, int64_t slot, int key, float w) {
+    const bool none = key == a.E;
+    a.dst[to] = (int)slot;
+    a.src[to] = none ? -1 : (int)(slot / a.k);
+    a.row_scale[to] = none ? 0.f : w;
+}
+// Exclusive sums of n counts in LDS over the workgroup's NT threads, in place; s_sum: a value per wave.
+template <int NT>
+__device__ __forceinline__ void exclusive_sums(int* s_n, int n, int* s_sum) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tiles = gridDim.x, tile = blockIdx.x, n = a.E + 1;
-    for (int e = lane; e < n; e += 64) s_at[wave][e] = 0;
-    wave_lds_order();
-    // each wave's own counts
-    const int64_t first = (int64_t)tile * kTileSlots + wave * PER;
-    for (int i = lane; i < PER; i += 64)
-        if (first + i < slots) atomicAdd(&s_at[wave][slot_key(a, first + i)], 1);
-    // all tiles' counts, and those of the tiles in front
-    int mine[(kMaxE + NT) / NT];
-#pragma unroll
-    for (int q = 0; q < (kMaxE + NT) / NT; ++q) {
-        const int e = tid + NT * q;
-        int all = 0;
-        mine[q] = 0;
-        if (e < n) {
-            for (int t = 0; t < tiles; ++t) {
-                const int h = hist[(int64_t)t * n + e];
-                all += h;
-                if (t < tile) mine[q] += h;
-            }
-            s_all[e] = all;
-        }
-    }
-    __syncthreads();
-    // exclusive sum of the counts over the experts: thread i takes a run of them
     const int run = (n + NT - 1) / NT, lo = min(n, tid * run), hi = min(n, lo + run);
     int sum = 0;
-    for (int e = lo; e < hi; ++e) sum += s_all[e];
+    for (int e = lo; e < hi; ++e) sum += s_n[e];
     int upto = sum;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -239,68 +473,181 @@ __global__ __launch_bounds__(64 * kPlanWaves) void route_place(const fqm_routing
     int at = upto - sum;
     for (int w = 0; w < wave; ++w) at += s_sum[w];
     for (int e = lo; e < hi; ++e) {
-        const int c = s_all[e];
-        s_all[e] = at;
+        const int c = s_n[e];
+        s_n[e] = at;
         at += c;
     }
     __syncthreads();
-    if (tile == 0)
+}
+
+// Workgroup b: tokens [b * tile, + tile), a wave each in turn.  hist: [tiles][E + 1], how many of the tile's slots go to
+// each expert and to none; NULL: not counted.
+constexpr int many_waves(int nv) { return nv <= 8 ? 16 : 8; }
+template <int NV, int NW>
+__global__ __launch_bounds__(64 * NW) void route_choose(const fqm_routing a, int tile, int* __restrict__ hist) {
+    constexpr int NT = 64 * NW;
+    __shared__ WaveLds<NV> s_wave[NW];
+    __shared__ int s_n[kMaxE + 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (hist) {
+        for (int e = tid; e <= a.E; e += NT) s_n[e] = 0;
+        __syncthreads();
+    }
+    const int64_t first = (int64_t)blockIdx.x * tile, end = min(first + tile, a.T);
+    choose_all<NV, NW>(a, first, end, &s_wave[wave], [&](int64_t t, int expert, float weight) {
+        if (lane >= a.k) return;
+        a.expert[t * a.k + lane] = expert;
+        a.weight[t * a.k + lane] = weight;
+        if (hist) atomicAdd(&s_n[key_of(a, expert)], 1);
+    });
+    if (hist) {
+        __syncthreads();
+        for (int e = tid; e <= a.E; e += NT) hist[(int64_t)blockIdx.x * (a.E + 1) + e] = s_n[e];
+    }
+}
+
+// The plan's rows of the slots of `span` tiles.  parts: a power of two, threads that share the counts of one expert.
+__global__ __launch_bounds__(64 * kPlaceWaves) void route_place(const fqm_routing a, const int* __restrict__ hist, int tile, int tiles,
+                                                                int span, int parts) {
+    constexpr int NW = kPlaceWaves, NT = 64 * NW;
+    __shared__ int s_all[kMaxE + 1];          // an expert's slots of all tiles, then its first row
+    __shared__ int s_front[kMaxE + 1];        // those of the tiles in front
+    __shared__ int s_at[NW][kMaxE + 1];       // its next row for each wave's slots
+    __shared__ int s_sum[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n = a.E + 1, here = (int)blockIdx.x * span;
+    const int64_t slots = a.T * a.k, first = (int64_t)here * tile * a.k, end = min(first + (int64_t)span * tile * a.k, slots);
+    for (int e = tid; e < n; e += NT) s_all[e] = s_front[e] = 0;
+    for (int e = lane; e < n; e += 64) s_at[wave][e] = 0;
+    __syncthreads();
+    // each wave's own counts, of its run of the tile's slots
+    const int64_t per = ((end - first + NW - 1) / NW + 63) / 64 * 64;
+    const int64_t lo = min(end, first + wave * per), hi = min(end, lo + per);
+    for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&s_at[wave][key_of(a, a.expert[i])], 1);
+    // all tiles' counts, and those in front: thread (e, q) takes the tiles q, q + parts, ...
+    const int stride = NT / parts, q = tid / stride;
+    for (int e = tid - q * stride; e < n; e += stride) {
+        int all = 0, front = 0;
+#pragma unroll 8
+        for (int t = q; t < tiles; t += parts) {
+            const int h = hist[(int64_t)t * n + e];
+            all += h;
+            front += t < here ? h : 0;
+        }
+        atomicAdd(&s_all[e], all);
+        atomicAdd(&s_front[e], front);
+    }
+    __syncthreads();
+    exclusive_sums<NT>(s_all, n, s_sum);
+    if (blockIdx.x == 0)
         for (int e = tid; e <= a.E; e += NT) a.offsets[e] = e < a.E ? s_all[e] : (int)slots;
-#pragma unroll
-    for (int q = 0; q < (kMaxE + NT) / NT; ++q) {
-        const int e = tid + NT * q;
-        if (e < n) {
-            int next = s_all[e] + mine[q];
-            for (int w = 0; w < kPlanWaves; ++w) {
-                const int c = s_at[w][e];
-                s_at[w][e] = next;
-                next += c;
-            }
+    for (int e = tid; e < n; e += NT) {
+        int next = s_all[e] + s_front[e];
+        for (int w = 0; w < NW; ++w) {
+            const int c = s_at[w][e];
+            s_at[w][e] = next;
+            next += c;
         }
     }
     __syncthreads();
-    for (int i0 = 0; i0 < PER; i0 += 64) {
-        const int64_t i = first + i0 + lane;
-        const bool live = i < slots;
-        const int key = live ? slot_key(a, i) : 0;
+    for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+        const int64_t i = i0 + lane;
+        const bool live = i < hi;
+        const int key = live ? key_of(a, a.expert[i]) : 0;
         const uint64_t peers = same_key(key, __ballot(live));
-        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(peers >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)peers, 0u));
-        if (live) {
-            const int to = s_at[wave][key] + before;
-            const bool none = key == a.E;
-            a.dst[to] = (int)i;
-            a.src[to] = none ? -1 : (int)(i / a.k);
-            a.row_scale[to] = none ? 0.f : a.weight[i];
-        }
+        const int before = lanes_before(peers);
+        if (live) place(a, s_at[wave][key] + before, i, key, a.weight[i]);
         wave_lds_order();
         if (live && before == 0) s_at[wave][key] += __builtin_popcountll(peers);
         wave_lds_order();
     }
 }
 
+// All of it for few tokens: at most 64 slots a wave.
+template <int NV>
+__global__ __launch_bounds__(64 * many_waves(NV)) void route_small(const fqm_routing a) {
+    constexpr int NW = many_waves(NV), NT = 64 * NW;
+    __shared__ WaveLds<NV> s_wave[NW];
+    __shared__ uint16_t s_at[NW][64 * NV + 2];  // a wave's slots of each expert, then those of the waves in front
+    __shared__ int s_n[64 * NV + 1], s_sum[NW];
+    __shared__ int s_key[NT];
+    __shared__ float s_w[NT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slots = (int)a.T * a.k, waves = (slots + 63) / 64;
+    for (int e = lane; e <= a.E; e += 64) s_at[wave][e] = 0;
+    choose_all<NV, NW>(a, 0, a.T, &s_wave[wave], [&](int64_t t, int expert, float weight) {
+        if (lane >= a.k) return;
+        const int i = (int)t * a.k + lane;
+        a.expert[i] = expert;
+        a.weight[i] = weight;
+        s_key[i] = key_of(a, expert);
+        s_w[i] = weight;
+    });
+    __syncthreads();
+    const bool live = tid < slots;
+    const int key = live ? s_key[tid] : 0;
+    const uint64_t peers = same_key(key, __ballot(live));
+    const int before = lanes_before(peers);
+    if (live && before == 0) s_at[wave][key] = (uint16_t)__builtin_popcountll(peers);
+    __syncthreads();
+    for (int e = tid; e <= a.E; e += NT) {
+        int n = 0;
+        for (int w = 0; w < waves; ++w) {
+            const int c = s_at[w][e];
+            s_at[w][e] = (uint16_t)n;
+            n += c;
+        }
+        s_n[e] = n;
+    }
+    __syncthreads();
+    exclusive_sums<NT>(s_n, a.E + 1, s_sum);
+    for (int e = tid; e <= a.E; e += NT) a.offsets[e] = e < a.E ? s_n[e] : slots;
+    if (live) place(a, s_n[key] + s_at[wave][key] + before, tid, key, s_w[tid]);
+}
+
+struct Tiles {
+    int64_t tile, n;  // tokens, tiles
+};
+Tiles tiles_of(const fqm_routing& a) {
+    const int64_t tile = std::max<int64_t>(1, (a.T + kFewWaves * kTiles - 1) / (kFewWaves * kTiles)) * kFewWaves;
+    return {tile, (a.T + tile - 1) / tile};
+}
+bool small(const fqm_routing& a) { return a.offsets && a.T <= kSmallTokens; }  // up to 64 * 8 slots
+
+template <int NV>
+hipError_t launch_nv(const fqm_routing& a, int* hist, hipStream_t s) {
+    constexpr int MW = many_waves(NV);
+    if (small(a)) {
+        hipLaunchKernelGGL(route_small<NV>, dim3(1), dim3(64 * MW), 0, s, a);
+        return hipGetLastError();
+    }
+    const Tiles t = tiles_of(a);
+    if (t.tile >= 2 * MW) hipLaunchKernelGGL((route_choose<NV, MW>), dim3((unsigned)t.n), dim3(64 * MW), 0, s, a, (int)t.tile, hist);
+    else hipLaunchKernelGGL((route_choose<NV, kFewWaves>), dim3((unsigned)t.n), dim3(64 * kFewWaves), 0, s, a, (int)t.tile, hist);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.offsets) return e;
+    int parts = 1;
+    while (parts < 16 && (a.E + 1) * parts * 2 <= 64 * kPlaceWaves) parts *= 2;
+    const int span = (int)std::max<int64_t>(1, 64 * kPlaceWaves / (t.tile * a.k));
+    hipLaunchKernelGGL(route_place, dim3((unsigned)((t.n + span - 1) / span)), dim3(64 * kPlaceWaves), 0, s, a, hist, (int)t.tile, (int)t.n,
+                       span, parts);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t route_workspace(const fqm_routing& a) {
-    if (!a.offsets) return 0;
-    const int64_t tiles = (a.T * a.k + kTileSlots - 1) / kTileSlots;
-    return ((size_t)tiles * (a.E + 1) * 4 + 15) / 16 * 16;
+    if (!a.offsets || small(a)) return 0;
+    return ((size_t)tiles_of(a).n * (a.E + 1) * 4 + 15) / 16 * 16;
 }
 
 hipError_t launch_route(const fqm_routing& a, void* ws, hipStream_t s) {
-    const int64_t slots = a.T * a.k, tiles = (slots + kTileSlots - 1) / kTileSlots;
-    const dim3 grid((unsigned)((a.T + kWaves - 1) / kWaves)), block(64 * kWaves);
-    if (a.E <= 64) hipLaunchKernelGGL(route_choose<1>, grid, block, 0, s, a);
-    else if (a.E <= 128) hipLaunchKernelGGL(route_choose<2>, grid, block, 0, s, a);
-    else if (a.E <= 256) hipLaunchKernelGGL(route_choose<4>, grid, block, 0, s, a);
-    else if (a.E <= 512) hipLaunchKernelGGL(route_choose<8>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(route_choose<16>, grid, block, 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.offsets) return e;
-    int* hist = static_cast<int*>(ws);
-    hipLaunchKernelGGL(route_count, dim3((unsigned)tiles), dim3(64 * kPlanWaves), 0, s, a, hist, slots);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(route_place, dim3((unsigned)tiles), dim3(64 * kPlanWaves), 0, s, a, hist, slots);
-    return hipGetLastError();
+    int* hist = a.offsets ? static_cast<int*>(ws) : nullptr;
+    if (a.E <= 64) return launch_nv<1>(a, hist, s);
+    if (a.E <= 128) return launch_nv<2>(a, hist, s);
+    if (a.E <= 256) return launch_nv<4>(a, hist, s);
+    if (a.E <= 512) return launch_nv<8>(a, hist, s);
+    return launch_nv<16>(a, hist, s);
 }
 
 }  // namespace fqm
