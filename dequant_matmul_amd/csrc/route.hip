@@ -24,16 +24,11 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kFewWaves = 4;         // of a choosing workgroup with a short tile
-constexpr int kTiles = 256;          // at most so many tiles
-constexpr int kPlaceWaves = 8;
+constexpr int kPlaceWaves = 16;
 constexpr int kSmallTokens = 8;      // one workgroup's work
 constexpr float kLargest = 3.4028234663852886e38f;
 
-__device__ __forceinline__ float logit(const fqm_routing& a, int64_t at) {
-    const float l = a.x_dtype == FQM_F32 ? static_cast<const float*>(a.logits)[at]
-                                         : bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at]);
-    return l > kLargest ? kLargest : l;  // a NaN stays one
-}
+__device__ __forceinline__ float held(float l) { return l > kLargest ? kLargest : l; }  // a NaN stays one
 // The sum over the wave in fp64, the same in every lane.
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ double dpp_add_f64(double x) {
@@ -49,6 +44,26 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     v = dpp_add_f64<0x140, 0xF>(v);
     v = dpp_add_f64<0x142, 0xA>(v);
     v = dpp_add_f64<0x143, 0xC>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// The largest of the wave's, the same in every lane.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_max_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)u, (int)u, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(u >> 32), (int)(u >> 32), CTRL, ROW_MASK, 0xF, false);
+    const double o = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    return o > x ? o : x;
+}
+__device__ __forceinline__ double wave_max_f64(double v) {
+    v = dpp_max_f64<0xB1, 0xF>(v);
+    v = dpp_max_f64<0x4E, 0xF>(v);
+    v = dpp_max_f64<0x141, 0xF>(v);
+    v = dpp_max_f64<0x140, 0xF>(v);
+    v = dpp_max_f64<0x142, 0xA>(v);
+    v = dpp_max_f64<0x143, 0xC>(v);
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
@@ -89,11 +104,17 @@ __device__ __forceinline__ double at_lane(double v, int l) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// A wave's token: its logits, its experts' biases, and which of them are open (bit v: expert lane + 64 v).
+// A wave's token: its logits, and which experts are open (bit v: expert lane + 64 v).
 template <int NV>
 struct Token {
-    float l[NV], b[NV];
+    float l[NV];
     uint32_t open;
+};
+// What does not change between tokens: the experts' biases, which experts may be chosen, their groups (8 bits each).
+template <int NV>
+struct Experts {
+    float b[NV];
+    uint32_t there, group[(NV + 3) / 4];
 };
 // What lane j < k has chosen: its expert (-1: none) and its logit.
 struct Chosen {
@@ -159,66 +180,77 @@ __device__ __forceinline__ uint64_t keep_groups(const fqm_routing& a, const V* c
     return kept;
 }
 
-// The choice with scores in fp64, for the few tokens that need it: from memory again, in loops, so that it takes no
-// registers from the others.  s_c: E values of LDS of the wave's own.
-__device__ __forceinline__ Chosen choose_exactly(const fqm_routing& a, int64_t row, double* s_c) {
+// A call: inlined, its constants would be kept in registers through all of the kernel.
+__device__ __attribute__((noinline)) double exp_f64(double x) { return exp(x); }
+
+// The choice with scores in fp64, for the few tokens that need it.  s_c: E values of LDS of the wave's own.  top and
+// z: the softmax's.
+template <int NV>
+__device__ __forceinline__ Chosen choose_exactly(const fqm_routing& a, const Token<NV>& t, const Experts<NV>& x, double* s_c,
+                                                 float* top_out, float* z_out) {
     const int lane = threadIdx.x & 63;
     const double kClosed = -INFINITY;
-    auto value = [&](int e) { return logit(a, row * a.ld_x + e); };
-    auto bias = [&](int e) { return a.bias ? a.bias[e] : 0.f; };
-    auto open = [&](int e) { return value(e) > -INFINITY && bias(e) > -INFINITY; };
-    double m = -(double)kLargest, z = 0.0;
-    if (a.score == FQM_SOFTMAX) {
-        float top = -kLargest;
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 64)
-            if (open(e)) top = fmaxf(top, value(e));
-        m = wave_max_f(top);
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 64)
-            if (open(e)) z += exp((double)value(e) - m);
-        z = wave_sum_f64(z);
+    const bool softmax = a.score == FQM_SOFTMAX;
+    float top = 0.f;
+    if (softmax) {
+        top = -kLargest;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (t.open >> v & 1) top = fmaxf(top, t.l[v]);
+        top = wave_max_f(top);
     }
-    auto score = [&](int e) {
-        const double l = value(e);
-        return a.score == FQM_SOFTMAX ? exp(l - m) / z : 1.0 / (1.0 + exp(-l));
-    };
-    const bool sums = a.groups > 1 && a.group_score == FQM_GROUP_TOP2;
-    uint64_t kept = ~0ull;
-    const int per = a.E / a.groups;
-    for (int pass = a.groups > 1 ? 0 : 1; pass < 2; ++pass) {  // the groups' values, then the experts'
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 64) {
-            double c = kClosed;
-            if (open(e) && (pass == 0 || kept >> (e / per & 63) & 1))
-                c = a.bias || (pass == 0 && sums) ? score(e) + (double)bias(e) : (double)value(e);
-            s_c[e] = c;
-        }
+    double c[NV], z = 0.0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        c[v] = exp_f64(softmax ? (double)t.l[v] - (double)top : -(double)t.l[v]);
+        if (t.open >> v & 1) z += c[v];
+    }
+    z = softmax ? wave_sum_f64(z) : 1.0;
+    *top_out = top;
+    *z_out = (float)z;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        c[v] = a.bias || (a.groups > 1 && a.group_score == FQM_GROUP_TOP2) ? softmax ? c[v] / z : 1.0 / (1.0 + c[v]) : (double)t.l[v];
+        c[v] = t.open >> v & 1 ? c[v] + (double)x.b[v] : kClosed;
+    }
+    if (a.groups > 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (lane + 64 * v < a.E) s_c[lane + 64 * v] = c[v];
         wave_lds_order();
-        if (pass == 0) {
-            bool near;
-            kept = keep_groups<double>(a, s_c, sums, 0.0, &near);
-            wave_lds_order();
+        bool near;
+        const uint64_t kept = keep_groups<double>(a, s_c, a.group_score == FQM_GROUP_TOP2, 0.0, &near);
+        wave_lds_order();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (!a.bias && t.open >> v & 1) c[v] = t.l[v];
+            if (!(kept >> (x.group[v / 4] >> 8 * (v & 3) & 63) & 1)) c[v] = kClosed;
         }
     }
     Chosen mine = {-1, 0.f};
     for (int j = 0; j < a.k; ++j) {
-        double bv = kClosed;
-        int be = kMaxE;
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 64)
-            if (s_c[e] > bv) bv = s_c[e], be = e;
+        double best = c[0];
 #pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            const double ov = __shfl_xor(bv, o, 64);
-            const int oi = __shfl_xor(be, o, 64);
-            if (ov > bv || (ov == bv && oi < be)) bv = ov, be = oi;
+        for (int v = 1; v < NV; ++v) best = c[v] > best ? c[v] : best;
+        best = wave_max_f64(best);
+        if (!(best > kClosed)) break;  // uniform
+        int e = kMaxE;
+#pragma unroll
+        for (int v = NV - 1; v >= 0; --v) {
+            const uint64_t at = __ballot(c[v] == best);
+            if (at) e = 64 * v + __builtin_ctzll(at);
         }
-        if (!(bv > kClosed)) break;  // uniform
-        if (lane == (be & 63)) s_c[be] = kClosed;
-        wave_lds_order();
-        if (lane == j) mine = {be, value(be)};
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (lane + 64 * v == e) c[v] = kClosed;
+        if (lane == j) mine.expert = e;
     }
+    float* s_l = reinterpret_cast<float*>(s_c);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) s_l[lane + 64 * v] = t.l[v];
+    wave_lds_order();
+    if (mine.expert >= 0) mine.l = s_l[mine.expert];
+    wave_lds_order();
     return mine;
 }
 
@@ -229,15 +261,37 @@ union WaveLds {
     double d[64 * NV];
 };
 
-// A token's expert and weight in lane j < k.
+// The weights of what lanes j < k have chosen; top and z: the softmax's largest logit and sum, where all of it counts.
+__device__ __forceinline__ float weigh(const fqm_routing& a, Chosen got, float top, float z) {
+    const bool softmax = a.score == FQM_SOFTMAX, live = got.expert >= 0 && (int)(threadIdx.x & 63) < a.k;
+    float w;
+    if (a.renormalise) {
+        // scores up to a common factor that keeps the largest away from zero: exp(l), or
+        // exp(min(l, 0)) / (1 + exp(-|l|))
+        const float e = softmax ? got.l : fminf(got.l, 0.f);
+        const float m = wave_max_f(live ? e : -INFINITY);
+        w = live ? exp_fast(e - m) : 0.f;
+        if (!softmax) w /= 1.f + exp_fast(-fabsf(got.l));
+        const float sum = wave_total(w);
+        w = sum > 0.f ? w / sum : 0.f;
+    } else if (softmax) {
+        const float d = got.l - top, t = d - got.l;
+        const float lost = (got.l - (d - t)) - (top + t);  // what d's rounding lost
+        w = exp_fast(d) * (1.f + fmaxf(-1.f, fminf(lost, 1.f))) / z;
+    } else {
+        w = logistic(got.l);
+    }
+    return live ? w * a.scale : 0.f;
+}
+
+// A token's experts in lanes j < k; false: fp32 leaves the choice open.
 template <int NV>
-__device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const Token<NV>& t, WaveLds<NV>* lds, int* expert,
-                                       float* weight) {
+__device__ __forceinline__ bool choose(const fqm_routing& a, const Token<NV>& t, const Experts<NV>& x, WaveLds<NV>* lds, Chosen* chosen,
+                                       float* top_out, float* z_out) {
     const int lane = threadIdx.x & 63;
     const bool sums = a.groups > 1 && a.group_score == FQM_GROUP_TOP2, softmax = a.score == FQM_SOFTMAX;
     const bool scored = a.bias || sums || (softmax && !a.renormalise);  // whether all scores are needed
-    float s[NV], c[NV], top = 0.f;
-    double z = 1.0;
+    float s[NV], c[NV], top = 0.f, z = 1.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) s[v] = 0.f;
     if (scored && softmax) {
@@ -252,8 +306,8 @@ __device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const 
             s[v] = t.open >> v & 1 ? exp_fast(t.l[v] - top) : 0.f;
             part += s[v];
         }
-        z = wave_sum_f64((double)part);
-        const float r = z > 0.0 ? 1.f / (float)z : 0.f;
+        z = wave_total(part);
+        const float r = z > 0.f ? 1.f / z : 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) s[v] *= r;
     } else if (scored) {
@@ -267,13 +321,13 @@ __device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const 
     if (a.bias) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (t.open >> v & 1) bmax = fmaxf(bmax, fabsf(t.b[v]));
+            if (t.open >> v & 1) bmax = fmaxf(bmax, fabsf(x.b[v]));
         bmax = wave_max_f(bmax);
     }
     uint32_t key[NV];  // 0: closed
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        c[v] = a.bias ? s[v] + t.b[v] : t.l[v];
+        c[v] = a.bias ? s[v] + x.b[v] : t.l[v];
         key[v] = t.open >> v & 1 ? ordered(c[v]) : 0u;
     }
     bool near = false;
@@ -287,22 +341,20 @@ __device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const 
         const float off = unit * (1.f + bmax);
         const uint64_t kept = keep_groups<float>(a, lds->f[0], sums, sums ? 2 * off : a.bias ? off : 0.f, &near);
         wave_lds_order();
-        const int per = a.E / a.groups;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int e = lane + 64 * v;
-            if (e < a.E && !(kept >> (e / per) & 1)) key[v] = 0u;
-        }
+        for (int v = 0; v < NV; ++v)
+            if (!(kept >> (x.group[v / 4] >> 8 * (v & 3) & 63) & 1)) key[v] = 0u;
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         lds->f[0][lane + 64 * v] = t.l[v];
         lds->f[1][lane + 64 * v] = c[v];
     }
-    // the k + 2 first, the j-th in lane j
+    // the k + 1 first, the j-th in lane j; without a bias the keys are the logits, whose order is exact
+    const int wanted = a.k + (a.bias ? 1 : 0);
     Chosen got = {-1, 0.f};
     int found = 0;
-    for (; found < a.k + 2; ++found) {
+    for (; found < wanted; ++found) {
         uint32_t m = key[0];
 #pragma unroll
         for (int v = 1; v < NV; ++v) m = max(m, key[v]);
@@ -326,111 +378,88 @@ __device__ __forceinline__ void choose(const fqm_routing& a, int64_t row, const 
         cj = lds->f[1][got.expert];
     }
     wave_lds_order();
-    if (a.bias && !near) {  // without a bias the keys are the logits
+    if (a.bias) {
         const float err = unit * (fabsf(at_lane(cj, 0)) + 2 * bmax);  // no score is larger than the first c and bmax
         const float cn = __shfl(cj, min(lane + 1, 63), 64);
-        const bool unsure = lane < min(a.k, found - 1) && !(cj - cn > 2 * err);
-        if (__ballot(unsure)) {
-            if (softmax) {
-                z = 0.0;
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (t.open >> v & 1) z += exp((double)t.l[v] - (double)top);
-                z = wave_sum_f64(z);
-            }
-            double exact = -INFINITY;
-            if (lane < found) {
-                const double l = got.l;
-                exact = (softmax ? exp(l - (double)top) / z : 1.0 / (1.0 + exp(-l))) + (double)a.bias[got.expert];
-            }
-            int rank = 0;
-            for (int o = 0; o < found; ++o) {
-                const double x = at_lane(exact, o);
-                const int e = __builtin_amdgcn_readlane(got.expert, o);
-                rank += x > exact || (x == exact && e < got.expert);
-            }
-            // what was not found is at most the last one's c and two errors: the k-th has to be above it
-            if (found == a.k + 2) {
-                const double kth = at_lane(exact, __builtin_ctzll(__ballot(lane < found && rank == a.k - 1)));
-                near = !(kth > (double)at_lane(cj, found - 1) + 2 * (double)err);
-            }
-            if (lane < found) {
-                lds->f[0][rank] = __int_as_float(got.expert);
-                lds->f[1][rank] = got.l;
-            }
-            wave_lds_order();
-            if (lane < found) {
-                got.expert = __float_as_int(lds->f[0][lane]);
-                got.l = lds->f[1][lane];
-            }
-            wave_lds_order();
-        }
+        near |= __ballot(lane < min(a.k, found - 1) && !(cj - cn > 2 * err)) != 0;
     }
-    if (near) got = choose_exactly(a, row, lds->d);
-
-    const bool live = got.expert >= 0 && lane < a.k;  // lanes k and k + 1 have the first that are not chosen
-    float w;
-    if (a.renormalise) {
-        // scores up to a common factor that keeps the largest away from zero: exp(l), or
-        // exp(min(l, 0)) / (1 + exp(-|l|))
-        const float e = softmax ? got.l : fminf(got.l, 0.f);
-        const float m = wave_max_f(live ? e : -INFINITY);
-        w = live ? expf(e - m) : 0.f;
-        if (!softmax) w /= 1.f + expf(-fabsf(got.l));
-        const float sum = wave_total(w);
-        w = sum > 0.f ? w / sum : 0.f;
-    } else {
-        w = softmax ? (float)(exp((double)got.l - (double)top) / z) : 1.f / (1.f + expf(-got.l));
-    }
-    *expert = got.expert;
-    *weight = live ? w * a.scale : 0.f;
+    *chosen = got;
+    *top_out = top;
+    *z_out = z;
+    return !near;
 }
 
 template <int NV>
-__device__ __forceinline__ void load_token(const fqm_routing& a, int64_t row, const float (&b)[NV], uint32_t there, Token<NV>* t) {
+__device__ __forceinline__ void load_token(const fqm_routing& a, int64_t row, Token<NV>* t) {
     const int lane = threadIdx.x & 63;
+    if (a.x_dtype == FQM_F32) {
+        const float* l = static_cast<const float*>(a.logits) + row * a.ld_x;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) t->l[v] = l[min(lane + 64 * v, a.E - 1)];
+    } else {
+        const uint16_t* l = static_cast<const uint16_t*>(a.logits) + row * a.ld_x;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) t->l[v] = bf16_to_f32(l[min(lane + 64 * v, a.E - 1)]);
+    }
+}
+// What is left to do once they have come.
+template <int NV>
+__device__ __forceinline__ void open_token(const Experts<NV>& x, Token<NV>* t) {
     t->open = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int e = lane + 64 * v;
-        t->l[v] = e < a.E ? logit(a, row * a.ld_x + e) : -INFINITY;
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        t->b[v] = b[v];
-        if ((there >> v & 1) && t->l[v] > -INFINITY) t->open |= 1u << v;
+        t->l[v] = held(t->l[v]);
+        if ((x.there >> v & 1) && t->l[v] > -INFINITY) t->open |= 1u << v;
     }
 }
-// The bias of a lane's experts; bit v of the answer: expert lane + 64 v may be chosen.
 template <int NV>
-__device__ __forceinline__ uint32_t load_bias(const fqm_routing& a, float (&b)[NV]) {
-    const int lane = threadIdx.x & 63;
-    uint32_t there = 0;
+__device__ __forceinline__ void load_experts(const fqm_routing& a, Experts<NV>* x) {
+    const int lane = threadIdx.x & 63, per = a.E / a.groups;
+    x->there = 0;
+#pragma unroll
+    for (int q = 0; q < (NV + 3) / 4; ++q) x->group[q] = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = lane + 64 * v;
-        b[v] = a.bias && e < a.E ? a.bias[e] : 0.f;
-        if (e < a.E && b[v] > -INFINITY) there |= 1u << v;
+        x->b[v] = a.bias && e < a.E ? a.bias[e] : 0.f;
+        if (e < a.E && x->b[v] > -INFINITY) x->there |= 1u << v;
+        if (e < a.E) x->group[v / 4] |= (uint32_t)(e / per) << 8 * (v & 3);
     }
-    return there;
 }
 
 // Chooses for the tokens first + wave, first + wave + NW, ... below end; the next one's logits are on their way meanwhile.
-// done(t, expert, weight): lane j < k has token t's j-th.
+// done(t, expert, weight): lane j < k has token t's j-th.  Tokens that fp32 leaves open wait until 64 are through.
 template <int NV, int NW, class Done>
 __device__ __forceinline__ void choose_all(const fqm_routing& a, int64_t first, int64_t end, WaveLds<NV>* lds, Done done) {
-    float b[NV];
-    const uint32_t there = load_bias<NV>(a, b);
-    int64_t t = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (t >= end) return;
-    Token<NV> token, next;
-    load_token<NV>(a, t, b, there, &token);
-    for (; t < end; t += NW, token = next) {
-        load_token<NV>(a, min(t + NW, end - 1), b, there, &next);
-        int expert;
-        float weight;
-        choose<NV>(a, t, token, lds, &expert, &weight);
-        done(t, expert, weight);
+    const int lane = threadIdx.x & 63;
+    for (int64_t t0 = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t0 < end; t0 += 64 * NW) {
+        Experts<NV> x;
+        load_experts<NV>(a, &x);
+        Token<NV> token, next;
+        load_token<NV>(a, t0, &token);
+        Chosen got;
+        float top, z;
+        uint64_t left = 0;
+        int64_t t = t0;
+        for (int r = 0; r < 64 && t < end; ++r, t += NW, token = next) {
+            load_token<NV>(a, min(t + NW, end - 1), &next);
+            open_token<NV>(x, &token);
+            if (choose<NV>(a, token, x, lds, &got, &top, &z)) {
+                const float w = weigh(a, got, top, z);
+                if (lane < a.k) done(t, got.expert, w);
+            } else {
+                left |= 1ull << r;
+            }
+        }
+        for (; left; left &= left - 1) {
+            t = t0 + NW * __builtin_ctzll(left);
+            load_experts<NV>(a, &x);
+            load_token<NV>(a, t, &token);
+            open_token<NV>(x, &token);
+            got = choose_exactly<NV>(a, token, x, lds->d, &top, &z);
+            const float w = weigh(a, got, top, z);
+            if (lane < a.k) done(t, got.expert, w);
+        }
     }
 }
 
@@ -480,83 +509,99 @@ __device__ __forceinline__ void exclusive_sums(int* s_n, int n, int* s_sum) {
     __syncthreads();
 }
 
-// Workgroup b: tokens [b * tile, + tile), a wave each in turn.  hist: [tiles][E + 1], how many of the tile's slots go to
-// each expert and to none; NULL: not counted.
+// Ints of a tile's counts: its slots' experts, those without one, and zeros up to whole uint4.
+__host__ __device__ __forceinline__ int counts_of(int E) { return (E + 4) / 4 * 4; }
+
+// Workgroup b: tokens [b * tile, + tile), a wave each in turn.  hist: the tiles' counts; NULL: not counted.
 constexpr int many_waves(int nv) { return nv <= 8 ? 16 : 8; }
+constexpr int min_waves(int nv) { return nv <= 4 ? 8 : 2; }  // a SIMD's, of launches that fill it
 template <int NV, int NW>
-__global__ __launch_bounds__(64 * NW) void route_choose(const fqm_routing a, int tile, int* __restrict__ hist) {
+__global__ __launch_bounds__(64 * NW, NW == kFewWaves ? 1 : min_waves(NV)) void route_choose(const fqm_routing a, int tile,
+                                                                                               int* __restrict__ hist) {
     constexpr int NT = 64 * NW;
     __shared__ WaveLds<NV> s_wave[NW];
-    __shared__ int s_n[kMaxE + 1];
+    __shared__ int s_n[64 * NV + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = counts_of(a.E);
     if (hist) {
-        for (int e = tid; e <= a.E; e += NT) s_n[e] = 0;
+        for (int e = tid; e < n; e += NT) s_n[e] = 0;
         __syncthreads();
     }
     const int64_t first = (int64_t)blockIdx.x * tile, end = min(first + tile, a.T);
     choose_all<NV, NW>(a, first, end, &s_wave[wave], [&](int64_t t, int expert, float weight) {
-        if (lane >= a.k) return;
         a.expert[t * a.k + lane] = expert;
         a.weight[t * a.k + lane] = weight;
         if (hist) atomicAdd(&s_n[key_of(a, expert)], 1);
     });
     if (hist) {
         __syncthreads();
-        for (int e = tid; e <= a.E; e += NT) hist[(int64_t)blockIdx.x * (a.E + 1) + e] = s_n[e];
+        for (int e = tid; e < n; e += NT) hist[(int64_t)blockIdx.x * n + e] = s_n[e];
     }
 }
 
-// The plan's rows of the slots of `span` tiles.  parts: a power of two, threads that share the counts of one expert.
+// The plan's rows of the slots of `span` tiles.
 __global__ __launch_bounds__(64 * kPlaceWaves) void route_place(const fqm_routing a, const int* __restrict__ hist, int tile, int tiles,
-                                                                int span, int parts) {
+                                                                int span) {
     constexpr int NW = kPlaceWaves, NT = 64 * NW;
-    __shared__ int s_all[kMaxE + 1];          // an expert's slots of all tiles, then its first row
-    __shared__ int s_front[kMaxE + 1];        // those of the tiles in front
+    __shared__ int s_all[kMaxE + 4];          // an expert's slots of all tiles, then its first row
+    __shared__ int s_front[kMaxE + 4];        // those of the tiles in front
     __shared__ int s_at[NW][kMaxE + 1];       // its next row for each wave's slots
     __shared__ int s_sum[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n = a.E + 1, here = (int)blockIdx.x * span;
+    const int n = counts_of(a.E), here = (int)blockIdx.x * span;
     const int64_t slots = a.T * a.k, first = (int64_t)here * tile * a.k, end = min(first + (int64_t)span * tile * a.k, slots);
-    for (int e = tid; e < n; e += NT) s_all[e] = s_front[e] = 0;
-    for (int e = lane; e < n; e += 64) s_at[wave][e] = 0;
-    __syncthreads();
-    // each wave's own counts, of its run of the tile's slots
     const int64_t per = ((end - first + NW - 1) / NW + 63) / 64 * 64;
     const int64_t lo = min(end, first + wave * per), hi = min(end, lo + per);
-    for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&s_at[wave][key_of(a, a.expert[i])], 1);
-    // all tiles' counts, and those in front: thread (e, q) takes the tiles q, q + parts, ...
-    const int stride = NT / parts, q = tid / stride;
-    for (int e = tid - q * stride; e < n; e += stride) {
-        int all = 0, front = 0;
+    const int key0 = lo + lane < hi ? key_of(a, a.expert[lo + lane]) : 0;  // the first 64 stay here
+    const float w0 = lo + lane < hi ? a.weight[lo + lane] : 0.f;
+    for (int e = tid; e < n; e += NT) s_all[e] = s_front[e] = 0;
+    for (int e = lane; e <= a.E; e += 64) s_at[wave][e] = 0;
+    __syncthreads();
+    // each wave's own counts, of its run of the slots
+    for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&s_at[wave][i < lo + 64 ? key0 : key_of(a, a.expert[i])], 1);
+    // all tiles' counts, and those in front: four experts a thread, of every step-th tile
+    const int quads = n / 4, step = NT / quads, q = tid % quads;
+    int all[4] = {}, front[4] = {};
+    if (tid < step * quads) {
 #pragma unroll 8
-        for (int t = q; t < tiles; t += parts) {
-            const int h = hist[(int64_t)t * n + e];
-            all += h;
-            front += t < here ? h : 0;
+        for (int t = tid / quads; t < tiles; t += step) {
+            const int4 h = reinterpret_cast<const int4*>(hist)[(int64_t)t * quads + q];
+            const int v[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all[i] += v[i];
+                front[i] += t < here ? v[i] : 0;
+            }
         }
-        atomicAdd(&s_all[e], all);
-        atomicAdd(&s_front[e], front);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            atomicAdd(&s_all[4 * q + i], all[i]);
+            atomicAdd(&s_front[4 * q + i], front[i]);
+        }
     }
     __syncthreads();
-    exclusive_sums<NT>(s_all, n, s_sum);
+    exclusive_sums<NT>(s_all, a.E + 1, s_sum);
     if (blockIdx.x == 0)
         for (int e = tid; e <= a.E; e += NT) a.offsets[e] = e < a.E ? s_all[e] : (int)slots;
-    for (int e = tid; e < n; e += NT) {
-        int next = s_all[e] + s_front[e];
+    for (int e = tid; e <= a.E; e += NT) {
+        int next = s_all[e] + s_front[e], c[NW];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) c[w] = s_at[w][e];
+#pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const int c = s_at[w][e];
             s_at[w][e] = next;
-            next += c;
+            next += c[w];
         }
     }
     __syncthreads();
     for (int64_t i0 = lo; i0 < hi; i0 += 64) {
         const int64_t i = i0 + lane;
         const bool live = i < hi;
-        const int key = live ? key_of(a, a.expert[i]) : 0;
+        const int key = i0 == lo ? key0 : live ? key_of(a, a.expert[i]) : 0;
+        const float w = i0 == lo ? w0 : live ? a.weight[i] : 0.f;
         const uint64_t peers = same_key(key, __ballot(live));
         const int before = lanes_before(peers);
-        if (live) place(a, s_at[wave][key] + before, i, key, a.weight[i]);
+        if (live) place(a, s_at[wave][key] + before, i, key, w);
         wave_lds_order();
         if (live && before == 0) s_at[wave][key] += __builtin_popcountll(peers);
         wave_lds_order();
@@ -576,7 +621,6 @@ __global__ __launch_bounds__(64 * many_waves(NV)) void route_small(const fqm_rou
     const int slots = (int)a.T * a.k, waves = (slots + 63) / 64;
     for (int e = lane; e <= a.E; e += 64) s_at[wave][e] = 0;
     choose_all<NV, NW>(a, 0, a.T, &s_wave[wave], [&](int64_t t, int expert, float weight) {
-        if (lane >= a.k) return;
         const int i = (int)t * a.k + lane;
         a.expert[i] = expert;
         a.weight[i] = weight;
@@ -609,7 +653,8 @@ struct Tiles {
     int64_t tile, n;  // tokens, tiles
 };
 Tiles tiles_of(const fqm_routing& a) {
-    const int64_t tile = std::max<int64_t>(1, (a.T + kFewWaves * kTiles - 1) / (kFewWaves * kTiles)) * kFewWaves;
+    const int64_t most = a.E <= 256 ? 512 : 256;  // tiles: two workgroups of 16 waves a compute unit fit up to 256 experts
+    const int64_t tile = std::max<int64_t>(1, (a.T + kFewWaves * most - 1) / (kFewWaves * most)) * kFewWaves;
     return {tile, (a.T + tile - 1) / tile};
 }
 bool small(const fqm_routing& a) { return a.offsets && a.T <= kSmallTokens; }  // up to 64 * 8 slots
@@ -626,11 +671,9 @@ hipError_t launch_nv(const fqm_routing& a, int* hist, hipStream_t s) {
     else hipLaunchKernelGGL((route_choose<NV, kFewWaves>), dim3((unsigned)t.n), dim3(64 * kFewWaves), 0, s, a, (int)t.tile, hist);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.offsets) return e;
-    int parts = 1;
-    while (parts < 16 && (a.E + 1) * parts * 2 <= 64 * kPlaceWaves) parts *= 2;
     const int span = (int)std::max<int64_t>(1, 64 * kPlaceWaves / (t.tile * a.k));
     hipLaunchKernelGGL(route_place, dim3((unsigned)((t.n + span - 1) / span)), dim3(64 * kPlaceWaves), 0, s, a, hist, (int)t.tile, (int)t.n,
-                       span, parts);
+                       span);
     return hipGetLastError();
 }
 
@@ -638,7 +681,7 @@ hipError_t launch_nv(const fqm_routing& a, int* hist, hipStream_t s) {
 
 size_t route_workspace(const fqm_routing& a) {
     if (!a.offsets || small(a)) return 0;
-    return ((size_t)tiles_of(a).n * (a.E + 1) * 4 + 15) / 16 * 16;
+    return (size_t)tiles_of(a).n * counts_of(a.E) * 4;
 }
 
 hipError_t launch_route(const fqm_routing& a, void* ws, hipStream_t s) {
