@@ -152,8 +152,8 @@ __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_nor
         for (int v = 0; v < NV; ++v) {
             const int c0 = kVec * (threadIdx.x + v * nt);
             if (n[v] > 0) {
-                if (f32) store_f32(a.total, tr + c0, h[v], n[v]);
-                else store_bf16(a.total, tr + c0, h[v], n[v]);
+                if (f32) store_f32(a.total, tr + c0, h[v], 0, n[v]);
+                else store_bf16(a.total, tr + c0, h[v], 0, n[v]);
             }
         }
     }
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_nor
             for (int i = 0; i < kVec; ++i)
                 c[i] = use ? (int)fminf(127.f, fmaxf(-127.f, rintf(w[v][i] * k * f))) : 0;
             const int c0 = kVec * (threadIdx.x + v * nt);
-            if (n[v] > 0) store_i8(a.y, yr + c0, c, n[v]);
+            if (n[v] > 0) store_i8(a.y, yr + c0, c, 0, n[v]);
         }
     } else {
 #pragma unroll
@@ -183,8 +183,8 @@ __global__ __launch_bounds__(kMaxThreads) void add_rms_norm_kernel(const fqm_nor
 #pragma unroll
             for (int i = 0; i < kVec; ++i) w[v][i] *= r;
             if (n[v] > 0) {
-                if (a.y_dtype == FQM_F32) store_f32(a.y, yr + c0, w[v], n[v]);
-                else store_bf16(a.y, yr + c0, w[v], n[v]);
+                if (a.y_dtype == FQM_F32) store_f32(a.y, yr + c0, w[v], 0, n[v]);
+                else store_bf16(a.y, yr + c0, w[v], 0, n[v]);
             }
         }
     }

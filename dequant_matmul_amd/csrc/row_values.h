@@ -55,10 +55,10 @@ struct Raw<true> {
     __device__ static float one(const void* p, int64_t e) { return static_cast<const float*>(p)[e]; }
 };
 
-// 8 values to p[e ...], n of them (8: one or two wide stores).
-__device__ __forceinline__ void store_f32(void* p, int64_t e, const float (&h)[kVec], int n) {
+// 8 values to p[e ...], those of [lo, hi) (all: one or two wide stores).
+__device__ __forceinline__ void store_f32(void* p, int64_t e, const float (&h)[kVec], int lo, int hi) {
     float* q = static_cast<float*>(p) + e;
-    if (n == kVec) {
+    if (lo == 0 && hi == kVec) {
         u32x4 a, b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -70,12 +70,12 @@ __device__ __forceinline__ void store_f32(void* p, int64_t e, const float (&h)[k
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (i < n) q[i] = h[i];
+            if (i >= lo && i < hi) q[i] = h[i];
     }
 }
-__device__ __forceinline__ void store_bf16(void* p, int64_t e, const float (&h)[kVec], int n) {
+__device__ __forceinline__ void store_bf16(void* p, int64_t e, const float (&h)[kVec], int lo, int hi) {
     uint16_t* q = static_cast<uint16_t*>(p) + e;
-    if (n == kVec) {
+    if (lo == 0 && hi == kVec) {
         u32x4 a;
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = (uint32_t)to_bf16(h[2 * i]) | (uint32_t)to_bf16(h[2 * i + 1]) << 16;
@@ -83,12 +83,12 @@ __device__ __forceinline__ void store_bf16(void* p, int64_t e, const float (&h)[
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (i < n) q[i] = to_bf16(h[i]);
+            if (i >= lo && i < hi) q[i] = to_bf16(h[i]);
     }
 }
-__device__ __forceinline__ void store_i8(void* p, int64_t e, const int (&c)[kVec], int n) {
+__device__ __forceinline__ void store_i8(void* p, int64_t e, const int (&c)[kVec], int lo, int hi) {
     uint8_t* q = static_cast<uint8_t*>(p) + e;
-    if (n == kVec) {
+    if (lo == 0 && hi == kVec) {
         u32x2 a;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -98,7 +98,7 @@ __device__ __forceinline__ void store_i8(void* p, int64_t e, const int (&c)[kVec
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (i < n) q[i] = (uint8_t)c[i];
+            if (i >= lo && i < hi) q[i] = (uint8_t)c[i];
     }
 }
 

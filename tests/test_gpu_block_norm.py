@@ -143,6 +143,43 @@ def test_results_do_not_depend_on_the_other_rows():
     assert torch.equal(a.y[77:78], b.y) and torch.equal(a.total[77:78], b.total)
 
 
+@pytest.mark.parametrize("cols", [2048, 2051, 5120, 8192])
+@pytest.mark.parametrize("x,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("gate", [None, "rows-bf16", "cols-bf16", "full-bf16"])
+def test_many_rows_have_the_bits_of_few(cols, x, res, gate):
+    c = case(1026, cols, 1, x, res, gate, pad=5)
+    c["weight"] = c["weight"].to(torch.bfloat16)
+    pick = [0, 5, 1025]
+    for out in (torch.float32, torch.int8):
+        a = fqm.block_norm(**c, out_dtype=out, gate_act="sigmoid" if gate else None)
+        few = {n: t[pick] if t is not None and t.dim() == 2 and t.shape[0] == 1026 else t for n, t in c.items()}
+        b = fqm.block_norm(**few, out_dtype=out, gate_act="sigmoid" if gate else None)
+        assert torch.equal(a.y[pick], b.y) and torch.equal(a.total[pick], b.total)
+        if out == torch.int8:
+            assert torch.equal(a.scale[pick], b.scale)
+    f = fqm.block_norm(**few, out_dtype=torch.float32, gate_act="sigmoid" if gate else None)
+    check(few, "f32", f, res, gate_act="sigmoid" if gate else None)
+
+
+@pytest.mark.parametrize("cols", [8192, 8193, 8200, 16384, 16391, 32768])
+@pytest.mark.parametrize("terms,gate", [(1, None), (3, "full-f32"), (9, "cols-bf16")])
+@pytest.mark.parametrize("out", ["f32", "i8"])
+def test_wide_rows(cols, terms, gate, out):
+    c = case(3, cols, terms, "bf16", "f32", gate)
+    check(c, out, fqm.block_norm(**c, out_dtype=T[out]), "f32")
+
+
+def test_total_in_place_of_the_residual_at_odd_widths():
+    """A row's last chunk starts in its neighbour's columns: their total may be stored by then."""
+    for cols in (9, 263, 1087, 2051, 8197):
+        c = case(1030, cols, 1, "bf16", "bf16", None)
+        c["post_weight"] = None
+        want = fqm.block_norm(**c, post=False)
+        r = c["residual"].clone()
+        got = fqm.block_norm(**dict(c, residual=r), post=False, total=r)
+        assert torch.equal(got.y, want.y) and torch.equal(r, want.total)
+
+
 def test_rows_of_zeros_and_what_is_not_finite():
     x = torch.randn(8, 200, device=DEV)
     r = torch.randn(8, 200, device=DEV)
