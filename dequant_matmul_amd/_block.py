@@ -161,22 +161,22 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tens
     T, E = logits.shape
     if out is not None:
         plan = out.offsets is not None
-    a = _routing_sizes(T, E, k, groups, top_groups, False)
-    a.logits, a.ld_x, a.x_dtype = logits.data_ptr(), _row_stride(logits, "logits", (T, E)), _CODE[logits.dtype]
-    a.score, a.group_score = _one_of(FQM_SCORE, score, "score"), _one_of(FQM_GROUP_SCORE, group_score, "group_score")
-    a.bias = _vector(bias, "bias", E, (torch.float32,), dev)
-    a.renormalise, a.scale = 1 if renormalise else 0, scale
-    if not 1 <= E <= 1024 or not 1 <= groups <= 64 or E % groups or not 1 <= a.top_groups <= groups:
-        raise ValueError(f"{E} experts (1 to 1024) in {groups} equal groups (1 to 64), of which {a.top_groups} stay")
-    if not 1 <= k <= min(32, E // groups * a.top_groups):
-        raise ValueError(f"k = {k}: 1 to 32 experts, as many as {a.top_groups} of {groups} groups of {E} hold at most")
+    if top_groups is None:
+        top_groups = groups
+    ld = _row_stride(logits, "logits", (T, E))
+    by, by_group = _one_of(FQM_SCORE, score, "score"), _one_of(FQM_GROUP_SCORE, group_score, "group_score")
+    added = _vector(bias, "bias", E, (torch.float32,), dev)
+    if not 1 <= E <= 1024 or not 1 <= groups <= 64 or E % groups or not 1 <= top_groups <= groups:
+        raise ValueError(f"{E} experts (1 to 1024) in {groups} equal groups (1 to 64), of which {top_groups} stay")
+    if not 1 <= k <= min(32, E // groups * top_groups):
+        raise ValueError(f"k = {k}: 1 to 32 experts, as many as {top_groups} of {groups} groups of {E} hold at most")
     n = T * k
     if out is None:
         ints = torch.empty(n * (3 if plan else 1) + (E + 1 if plan else 0), dtype=torch.int32, device=dev)
         floats = torch.empty(n * (2 if plan else 1), dtype=torch.float32, device=dev)
         if plan:
-            expert, src, dst, offsets = ints.split((n, n, n, E + 1))
-            weight, row_scale = floats.split((n, n))
+            expert, src, dst, offsets = ints.split_with_sizes((n, n, n, E + 1))
+            weight, row_scale = floats.split_with_sizes((n, n))
             out = Routing(expert.view(T, k), weight.view(T, k), offsets, src, dst, row_scale)
         else:
             out = Routing(ints.view(T, k), floats.view(T, k), None, None, None, None)
@@ -189,10 +189,9 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tens
             _need(t, f"out.{name}", (dt,), dev)
             if tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"out.{name} has shape {tuple(t.shape)}; expected contiguous {shape}")
-    a.expert, a.weight = out.expert.data_ptr(), out.weight.data_ptr()
-    if plan:
-        a.offsets, a.src, a.dst = out.offsets.data_ptr(), out.src.data_ptr(), out.dst.data_ptr()
-        a.row_scale = out.row_scale.data_ptr()
+    rest = (out.offsets.data_ptr(), out.src.data_ptr(), out.dst.data_ptr(), out.row_scale.data_ptr()) if plan else ()
+    a = _Routing(T, E, k, logits.data_ptr(), ld, _CODE[logits.dtype], by, added, groups, top_groups, by_group,
+                 1 if renormalise else 0, scale, out.expert.data_ptr(), out.weight.data_ptr(), *rest)
     _check_workspace(workspace, dev)
     lib = load()
     if workspace is None:
@@ -240,40 +239,33 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_weigh
         raise ValueError(f"x has {terms} terms; 1 to 64 can be added up")
     if cols > 1 and x.stride(-1) != 1:
         raise ValueError("x must have dense rows (stride 1 in the last dimension)")
-    a = _Block()
-    a.rows, a.cols, a.terms, a.post, a.x_dtype = rows, cols, terms, 1 if post else 0, _CODE[x.dtype]
-    a.eps, a.weight_offset, a.scale, a.residual_scale = eps, weight_offset, scale, residual_scale
-    a.x, a.ld_x, a.ld_term = x.data_ptr(), x.stride(0) if rows > 1 else cols, x.stride(1) if terms > 1 else cols
-    if a.ld_x < cols or a.ld_term < cols:
+    ld_x, ld_term = x.stride(0) if rows > 1 else cols, x.stride(1) if terms > 1 else cols
+    if ld_x < cols or ld_term < cols:
         raise ValueError("x has overlapping rows")
+    ld_res = ld_gate = step_gate = ld_total = ld_y = res_dtype = gate_dtype = 0
     total_dtype = x.dtype
     if residual is not None:
         _need(residual, "residual", _VALUE, dev)
-        a.ld_res = _row_stride(residual, "residual", (rows, cols))
+        ld_res = _row_stride(residual, "residual", (rows, cols))
         total_dtype = residual.dtype
-        a.residual, a.res_dtype = residual.data_ptr(), _CODE[total_dtype]
-    if post_weight is not None:
-        if not post:
-            raise ValueError("post_weight belongs to the norm that post=False leaves out")
-        a.post_weight = _vector(post_weight, "post_weight", cols, _VALUE, dev)
-        a.post_dtype = _CODE[post_weight.dtype]
-    if weight is not None:
-        a.weight = _vector(weight, "weight", cols, _VALUE, dev)
-        a.weight_dtype = _CODE[weight.dtype]
-    a.gate_act = _one_of(FQM_ACT, gate_act, "gate_act")
+        res_dtype = _CODE[total_dtype]
+    if post_weight is not None and not post:
+        raise ValueError("post_weight belongs to the norm that post=False leaves out")
+    w1, w2 = _vector(post_weight, "post_weight", cols, _VALUE, dev), _vector(weight, "weight", cols, _VALUE, dev)
+    act = _one_of(FQM_ACT, gate_act, "gate_act")
     if gate is not None:
         _need(gate, "gate", _VALUE, dev)
-        a.gate, a.gate_dtype = gate.data_ptr(), _CODE[gate.dtype]
+        gate_dtype = _CODE[gate.dtype]
         if gate.dim() == 1 and gate.shape[0] == cols:
             if cols > 1 and gate.stride(0) != 1:
                 raise ValueError("gate must be dense (stride 1 in the last dimension)")
-            a.ld_gate, a.step_gate = 0, 1
+            step_gate = 1
         elif gate.dim() == 2 and gate.shape[0] == rows and gate.shape[1] in (1, cols):
-            a.step_gate = 0 if gate.shape[1] == 1 else 1
-            if a.step_gate and cols > 1 and gate.stride(1) != 1:
+            step_gate = 0 if gate.shape[1] == 1 else 1
+            if step_gate and cols > 1 and gate.stride(1) != 1:
                 raise ValueError("gate must have dense rows (stride 1 in the last dimension)")
-            a.ld_gate = gate.stride(0) if rows > 1 else 0
-            if a.ld_gate and a.ld_gate < gate.shape[1]:
+            ld_gate = gate.stride(0) if rows > 1 else 0
+            if ld_gate and ld_gate < gate.shape[1]:
                 raise ValueError("gate has overlapping rows")
         else:
             raise ValueError(f"gate has shape {tuple(gate.shape)}; expected ({cols},), ({rows}, 1) or ({rows}, {cols})")
@@ -281,27 +273,30 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_weigh
         raise ValueError("gate_act without a gate")
     if total is not None:
         _need(total, "total", (total_dtype,), dev)
-        a.ld_total, a.total = _row_stride(total, "total", (rows, cols)), total.data_ptr()
+        ld_total = _row_stride(total, "total", (rows, cols))
     elif keep_total:
         total = torch.empty((rows, cols), dtype=total_dtype, device=dev)
-        a.ld_total, a.total = cols, total.data_ptr()
+        ld_total = cols
     if y is None and out_dtype is not None:
         if out_dtype not in _CODE:
             raise ValueError(f"out_dtype must be bfloat16, float32, int8 or None, not {out_dtype}")
         y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-        a.ld_y = cols
+        ld_y = cols
     elif y is not None:
         _need(y, "y", tuple(_CODE), dev)
-        a.ld_y = _row_stride(y, "y", (rows, cols))
+        ld_y = _row_stride(y, "y", (rows, cols))
     if y is None and total is None:
         raise ValueError("nothing to compute: neither y nor total is asked for")
-    if y is not None:
-        a.y, a.y_dtype = y.data_ptr(), _CODE[y.dtype]
     if y is not None and y.dtype == torch.int8:
         if y_scale is None:
             y_scale = torch.empty(rows, dtype=torch.float32, device=dev)
-        a.y_scale = _vector(y_scale, "y_scale", rows, (torch.float32,), dev)
+        _vector(y_scale, "y_scale", rows, (torch.float32,), dev)
     else:
         y_scale = None
+    a = _Block(rows, cols, terms, 1 if post else 0, _CODE[x.dtype], res_dtype, 0 if w1 is None else _CODE[post_weight.dtype],
+               0 if w2 is None else _CODE[weight.dtype], gate_dtype, 0 if y is None else _CODE[y.dtype], act, eps, weight_offset,
+               scale, residual_scale, x.data_ptr(), ld_x, ld_term, w1, None if gate is None else gate.data_ptr(), ld_gate, step_gate,
+               None if residual is None else residual.data_ptr(), ld_res, w2, None if total is None else total.data_ptr(), ld_total,
+               None if y is None else y.data_ptr(), ld_y, None if y_scale is None else y_scale.data_ptr())
     _check(load().fqm_block_norm(ctypes.byref(a), _handle(dev)), "fqm_block_norm")
     return NormOut(y, y_scale, total)
