@@ -4,16 +4,21 @@
 //
 // Choice: one wave per token, expert e on lane e mod 64.  An expert's score + bias (its logit, without
 // a bias) in fp32, as an integer of the same order, is a key; a choice is a maximum over the wave (six DPP
-// instructions) and, of the lanes that have it, the lowest expert.  Two more than k are chosen.  Where
-// fp32's errors leave the order of the first k + 1 open (one token in some hundreds), the chosen ones' scores
-// are formed again in fp64, a lane each, and ranked; where they leave open even which these are, all
-// experts' are.
+// instructions) and, of the lanes that have it, the lowest expert.  One more than k are chosen with a bias.
+// Where fp32's errors leave the order of these open, or which groups stay (one token in some hundreds), the
+// token is put off until the wave's others are through, and chosen from scores in fp64: inside the
+// loop that path's registers would cost every token its neighbours' waves.
 //
-// Plan: up to kTiles tiles of tokens count their experts as they choose; a second launch
+// Plan: up to kMostTiles tiles of tokens count their experts as they choose; a second launch
 // adds up the counts of the tiles in front of each, and ranks its slots wave by wave: lanes
 // with the same expert find each other with one ballot per bit of its number.  No
 // counter is taken by whoever comes first, so the order of a group's rows is the slots'
-// order, whatever the timing.  Few tokens are one workgroup's work, in one launch.
+// order, whatever the timing.  The fewest tokens are one workgroup's work, in one launch.
+//
+// What binds it, on one MI355X: the issue of some 780 vector and 530 scalar instructions a token (256 experts, 8
+// groups, k 8) and the waits between dependent ones, for many tokens (16384: 29 us, and 13 us for the
+// plan, whose workgroups each read all tiles' counts); launches and the latency of one token's chain of steps
+// for few (1 token 5.6 us, 48 tokens 13.5 us in two launches).
 #include <algorithm>
 
 #include "activation.h"
@@ -24,8 +29,10 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kFewWaves = 4;         // of a choosing workgroup with a short tile
+constexpr int kMostTiles = 512;
 constexpr int kPlaceWaves = 16;
-constexpr int kSmallTokens = 8;      // one workgroup's work
+constexpr int kSmallTokens = 8;      // one workgroup's work: 8 tokens of 256 experts 10.8 us, 9 in two launches 12.1; on
+                                     // one compute unit 16 tokens take 13.1, as in two launches, 48 take 27, in two 13.5
 constexpr float kLargest = 3.4028234663852886e38f;
 
 __device__ __forceinline__ float held(float l) { return l > kLargest ? kLargest : l; }  // a NaN stays one
@@ -427,7 +434,7 @@ __device__ __forceinline__ void load_experts(const fqm_routing& a, Experts<NV>* 
     }
 }
 
-// Chooses for the tokens first + wave, first + wave + NW, ... below end; the next one's logits are on their way meanwhile.
+// Chooses for the tokens first + wave, first + wave + NW, ... below end.
 // done(t, expert, weight): lane j < k has token t's j-th.  Tokens that fp32 leaves open wait until 64 are through.
 template <int NV, int NW, class Done>
 __device__ __forceinline__ void choose_all(const fqm_routing& a, int64_t first, int64_t end, WaveLds<NV>* lds, Done done) {
@@ -435,14 +442,13 @@ __device__ __forceinline__ void choose_all(const fqm_routing& a, int64_t first, 
     for (int64_t t0 = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t0 < end; t0 += 64 * NW) {
         Experts<NV> x;
         load_experts<NV>(a, &x);
-        Token<NV> token, next;
-        load_token<NV>(a, t0, &token);
+        Token<NV> token;
         Chosen got;
         float top, z;
         uint64_t left = 0;
         int64_t t = t0;
-        for (int r = 0; r < 64 && t < end; ++r, t += NW, token = next) {
-            load_token<NV>(a, min(t + NW, end - 1), &next);
+        for (int r = 0; r < 64 && t < end; ++r, t += NW) {
+            load_token<NV>(a, t, &token);
             open_token<NV>(x, &token);
             if (choose<NV>(a, token, x, lds, &got, &top, &z)) {
                 const float w = weigh(a, got, top, z);
@@ -513,8 +519,10 @@ __device__ __forceinline__ void exclusive_sums(int* s_n, int n, int* s_sum) {
 __host__ __device__ __forceinline__ int counts_of(int E) { return (E + 4) / 4 * 4; }
 
 // Workgroup b: tokens [b * tile, + tile), a wave each in turn.  hist: the tiles' counts; NULL: not counted.
-constexpr int many_waves(int nv) { return nv <= 8 ? 16 : 8; }
-constexpr int min_waves(int nv) { return nv <= 4 ? 8 : 2; }  // a SIMD's, of launches that fill it
+// The waves of a workgroup with a long tile, and what two such workgroups make of them on a SIMD, where registers allow:
+// 256 experts need 77, which 16 waves would spill (16384 tokens 36 us, with 12 waves 29).
+constexpr int many_waves(int nv) { return nv <= 2 ? 16 : nv <= 4 ? 12 : nv <= 8 ? 16 : 8; }
+constexpr int min_waves(int nv) { return nv <= 2 ? 8 : nv <= 4 ? 6 : 2; }
 template <int NV, int NW>
 __global__ __launch_bounds__(64 * NW, NW == kFewWaves ? 1 : min_waves(NV)) void route_choose(const fqm_routing a, int tile,
                                                                                                int* __restrict__ hist) {
@@ -653,7 +661,7 @@ struct Tiles {
     int64_t tile, n;  // tokens, tiles
 };
 Tiles tiles_of(const fqm_routing& a) {
-    const int64_t most = a.E <= 256 ? 512 : 256;  // tiles: two workgroups of 16 waves a compute unit fit up to 256 experts
+    const int64_t most = a.E <= 256 ? kMostTiles : kMostTiles / 2;  // up to 256 experts two workgroups fit a compute unit
     const int64_t tile = std::max<int64_t>(1, (a.T + kFewWaves * most - 1) / (kFewWaves * most)) * kFewWaves;
     return {tile, (a.T + tile - 1) / tile};
 }
@@ -667,7 +675,8 @@ hipError_t launch_nv(const fqm_routing& a, int* hist, hipStream_t s) {
         return hipGetLastError();
     }
     const Tiles t = tiles_of(a);
-    if (t.tile >= 2 * MW) hipLaunchKernelGGL((route_choose<NV, MW>), dim3((unsigned)t.n), dim3(64 * MW), 0, s, a, (int)t.tile, hist);
+    // 8192 tokens of 256 experts 39 us with 4 waves, 31 with 12; 48 tokens 13.5 with 4
+    if (t.tile >= MW) hipLaunchKernelGGL((route_choose<NV, MW>), dim3((unsigned)t.n), dim3(64 * MW), 0, s, a, (int)t.tile, hist);
     else hipLaunchKernelGGL((route_choose<NV, kFewWaves>), dim3((unsigned)t.n), dim3(64 * kFewWaves), 0, s, a, (int)t.tile, hist);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.offsets) return e;
