@@ -8,8 +8,9 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-// y as it is (PlainOut) or fqm_linear's epilogue (LinearOut).  row(group, r, per): the row of W of wave r of `per` in workgroup `group`, some row past the end; x_at(b, k):
-// batch row b's k-th 16-byte piece of x; done(...): lane 63 of wave r holds the sums.
+// y as it is (PlainOut) or fqm_linear's epilogue (LinearOut).  row(group, r, per): the row of W of wave r of `per` in
+// workgroup `group`, some row past the end; x_piece(t): x's t-th 16-byte piece, all batch rows as one; done(...): lane
+// 63 of wave r holds the sums.
 struct PlainOut {
     const uint16_t* x;
     void* y;

@@ -5,7 +5,14 @@
 // is two stacked matrices, a wave's 32 rows of W are 16 of the first and the same
 // 16 of the second, so that both factors of an output are in the same wave.
 // Few tiles are split along K; the parts' sums go through the workspace and a
-// second launch adds them in order and applies the epilogue.
+// second launch adds them in order and applies the epilogue.  Up to 32 rows the weights' stream is the
+// work, and other kernels do it: a wave a row of W for one to three rows, 16-row blocks up to eight (the
+// gemv kernels with this epilogue), the stream kernel below beyond.
+//
+// What binds it, on one MI355X: the matrix cores and the tables' gathers beside them for many rows (2048 rows 5120 ->
+// 8704 gated 361 us, 1.01 PFLOP/s, of which the epilogue and the partial round's two launches are 60), the
+// weights' stream for few (1 row 17408 -> 5120 15.6 us, 4.3 TB/s of codes and tables; 16 rows 5120 -> 17408 gated
+// 42 us and 5 for the sums), launches and the parts' way through memory between (77 rows 4160 -> 1000 8.7 + 4.9 us).
 #include <algorithm>
 
 #include "linear.h"
@@ -158,10 +165,10 @@ __global__ __launch_bounds__(256) void linear_reduce(const Linear p, const float
 
 // ---- up to 32 rows -----------------------------------------------------------------------
 // Here the weights' stream is the work.  A workgroup's 4 waves own 32 rows of W each and share the
-// rows of X; K goes by in stages of 128.  Codes and X come by direct global -> LDS loads, two stages
-// ahead in a ring of three, in whole 64-byte pieces of a row: read straight into the operands' layout
-// (24 bytes a lane, a row of W on every second lane) the codes cost the address unit 128 accesses for 2 KB
-// and bound the kernel at 28 us for 69 MB; this way they cost 24.
+// rows of X; K goes by in stages of 128.  Codes and X come by direct global -> LDS loads, a stage
+// ahead (a third buffer gained nothing: two workgroups a compute unit cover each other's waits), in whole 64-byte
+// pieces of a row: read straight into the operands' layout (24 bytes a lane, a row of W on every second lane) the
+// codes cost the address unit 128 accesses for 2 KB and bound the kernel at 28 us for 69 MB; this way they cost 24.
 //
 // All tiles' stages are one range, cut evenly over the workgroups (two a compute unit): each has the same
 // work whatever the shape, and at most two tiles that it shares with others.  Their sums go through the
@@ -584,6 +591,8 @@ Linear linear_of(const fqm_weights& w, const fqm_epilogue& a) {
     return p;
 }
 
+// Measured: 1 row 17408 -> 5120 15.6 us on a wave a row and 31 on the tiles; 8 rows 5120 -> 17408 24 us in 16-row blocks,
+// 27 on the stream kernel; 16 rows 5120 -> 17408 gated 47 us on the stream kernel, 66 on the tiles.
 enum class Path { rows, mfma, stream, tiles };
 Path path_of(const fqm_weights& w, const Linear& p) {
     if (p.a.M <= 3 && (w.format == FQM_LUT6 ? lut6_gemv_rows_path(w, (int)p.a.M) : lut4_gemv_rows_path(w, (int)p.a.M))) return Path::rows;
