@@ -80,6 +80,38 @@ def test_a_long_prompt():
     assert np.array_equal(r.expert[pick].cpu().numpy(), o["expert"])
 
 
+@pytest.mark.parametrize("E", [24, 100, 256, 500, 1000])
+@pytest.mark.parametrize("tokens", [1500, 4100, 9000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens_by_the_number_of_experts(tokens, E, score):
+    """Every 16th token's scores are within 1e-6 of each other, biased: what fp32 leaves open is taken up after the
+    others.  The plan against a stable sort, the choice against the definition and against a call of few tokens."""
+    print(f"route {tokens}x{E} {score}", flush=True)
+    rng = np.random.default_rng([tokens, E])
+    l = rng.standard_normal(E).astype(np.float32)
+    s = 1 / (1 + np.exp(-l.astype(np.float64))) if score == "sigmoid" else np.exp(l.astype(np.float64)) / np.exp(l.astype(np.float64)).sum()
+    bias = torch.from_numpy((0.9 - s).astype(np.float32)).to(DEV)
+    rows = rng.standard_normal((tokens, E)).astype(np.float32)
+    rows[::16] = l
+    rows[32] = -np.inf
+    logits = torch.from_numpy(rows).to(DEV)
+    kw = dict(score=score, bias=bias, groups=4, top_groups=3, group_score="top2")
+    r = fqm.route(logits, 6, **kw)
+    key = torch.where(r.expert < 0, E, r.expert).flatten()
+    order = torch.argsort(key, stable=True)
+    assert torch.equal(r.dst, order.int())
+    assert torch.equal(r.src, torch.where(key[order] < E, order // 6, -1).int())
+    counts = torch.bincount(key, minlength=E + 1)
+    counts[E - 1] += counts[E]
+    assert torch.equal(r.offsets.diff(), counts[:E].int()) and r.offsets[0] == 0
+    assert torch.equal(r.row_scale, r.weight.flatten()[order])
+    pick = torch.tensor([0, 1, 16, 31, 32, tokens // 16 * 16 - 16, tokens - 2, tokens - 1], device=DEV)
+    few = run(logits[pick].contiguous(), 6, **kw)
+    got = fqm.route(logits[pick].contiguous(), 6, **kw)
+    assert np.array_equal(r.expert[pick].cpu().numpy(), few["expert"])
+    assert torch.equal(r.expert[pick], got.expert) and torch.equal(r.weight[pick], got.weight)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("gs", ["max", "top2"])
 def test_ties_go_to_the_lowest_index(score, gs):
