@@ -268,6 +268,12 @@ union WaveLds {
     double d[64 * NV];
 };
 
+// exp(l - top) with what the difference's rounding lost.
+__device__ __forceinline__ float exp_below(float l, float top) {
+    const float d = l - top, t = d - l;
+    const float lost = (l - (d - t)) - (top + t);
+    return exp_fast(d) * (1.f + fmaxf(-1.f, fminf(lost, 1.f)));
+}
 // The weights of what lanes j < k have chosen; top and z: the softmax's largest logit and sum, where all of it counts.
 __device__ __forceinline__ float weigh(const fqm_routing& a, Chosen got, float top, float z) {
     const bool softmax = a.score == FQM_SOFTMAX, live = got.expert >= 0 && (int)(threadIdx.x & 63) < a.k;
@@ -277,14 +283,12 @@ __device__ __forceinline__ float weigh(const fqm_routing& a, Chosen got, float t
         // exp(min(l, 0)) / (1 + exp(-|l|))
         const float e = softmax ? got.l : fminf(got.l, 0.f);
         const float m = wave_max_f(live ? e : -INFINITY);
-        w = live ? exp_fast(e - m) : 0.f;
-        if (!softmax) w /= 1.f + exp_fast(-fabsf(got.l));
+        w = live ? expf(e - m) : 0.f;
+        if (!softmax) w /= 1.f + expf(-fabsf(got.l));
         const float sum = wave_total(w);
         w = sum > 0.f ? w / sum : 0.f;
     } else if (softmax) {
-        const float d = got.l - top, t = d - got.l;
-        const float lost = (got.l - (d - t)) - (top + t);  // what d's rounding lost
-        w = exp_fast(d) * (1.f + fmaxf(-1.f, fminf(lost, 1.f))) / z;
+        w = exp_below(got.l, top) / z;
     } else {
         w = logistic(got.l);
     }
@@ -307,13 +311,13 @@ __device__ __forceinline__ bool choose(const fqm_routing& a, const Token<NV>& t,
         for (int v = 0; v < NV; ++v)
             if (t.open >> v & 1) top = fmaxf(top, t.l[v]);
         top = wave_max_f(top);
-        float part = 0.f;
+        double part = 0.0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            s[v] = t.open >> v & 1 ? exp_fast(t.l[v] - top) : 0.f;
-            part += s[v];
+            s[v] = t.open >> v & 1 ? exp_below(t.l[v], top) : 0.f;
+            part += (double)s[v];
         }
-        z = wave_total(part);
+        z = (float)wave_sum_f64(part);
         const float r = z > 0.f ? 1.f / z : 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) s[v] *= r;
@@ -321,9 +325,9 @@ __device__ __forceinline__ bool choose(const fqm_routing& a, const Token<NV>& t,
 #pragma unroll
         for (int v = 0; v < NV; ++v) s[v] = logistic(t.l[v]);
     }
-    // How far s + bias may be off, U = 2^-24: 7 U of a sigmoid and U of the sum; of a softmax 4 U for the exponential, U
-    // for its argument, 16 U and what the exponentials have for z, 3 U for the product.
-    const float unit = softmax ? 0x1p-18f : 0x1p-20f;
+    // How far s + bias may be off, U = 2^-24: 7 U of a sigmoid and U of the sum; of a softmax 6 U for the exponential,
+    // as many and U for z, 4 U for its reciprocal and the product.
+    const float unit = softmax ? 0x1p-19f : 0x1p-20f;
     float bmax = 0.f;
     if (a.bias) {
 #pragma unroll
