@@ -592,11 +592,15 @@ Linear linear_of(const fqm_weights& w, const fqm_epilogue& a) {
 }
 
 // Measured: 1 row 17408 -> 5120 15.6 us on a wave a row and 31 on the tiles; 8 rows 5120 -> 17408 24 us in 16-row blocks,
-// 27 on the stream kernel; 16 rows 5120 -> 17408 gated 47 us on the stream kernel, 66 on the tiles.
+// 27 on the stream kernel; 16 rows 5120 -> 17408 gated 47 us on the stream kernel, 66 on the tiles.  Three rows, a wave
+// a row of W / 16-row blocks: 4-bit 2048 -> 4096 4.7 / 10.1, 5120 -> 17408 23.5 / 20.7, 9216 -> 17297 41 / 32 (6-bit 4.8 /
+// 10.6, 24.7 / 24.1, 44 / 39); two rows 9216 -> 17297 27 / 32 (6-bit 32 / 38).
 enum class Path { rows, mfma, stream, tiles };
 Path path_of(const fqm_weights& w, const Linear& p) {
+    const bool blocks = p.a.M <= 8 && lut_gemv_mfma_supported(w, (int)std::max<int64_t>(p.a.M, 2));
+    if (blocks && p.a.M >= 3 && w.rows * w.cols >= 1 << 26) return Path::mfma;
     if (p.a.M <= 3 && (w.format == FQM_LUT6 ? lut6_gemv_rows_path(w, (int)p.a.M) : lut4_gemv_rows_path(w, (int)p.a.M))) return Path::rows;
-    if (p.a.M <= 8 && lut_gemv_mfma_supported(w, (int)std::max<int64_t>(p.a.M, 2))) return Path::mfma;
+    if (blocks) return Path::mfma;
     return stream_path(p) ? Path::stream : Path::tiles;
 }
 }  // namespace
