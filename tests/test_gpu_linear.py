@@ -98,7 +98,8 @@ def test_output_counts_around_the_tiles(M, K, n, gated):
     run_case(6 if n % 2 else 4, M, K, n, gated, "silu", "bf16", "bf16", "f32", pad=1, seed=n)
 
 
-@pytest.mark.parametrize("M,K,n", [(1, 5120, 17408), (16, 5120, 9000), (3, 1024, 17000), (5, 1024, 33000), (64, 512, 17408)])
+@pytest.mark.parametrize("M,K,n", [(1, 5120, 17408), (16, 5120, 9000), (3, 1024, 17000), (3, 5120, 14000), (5, 1024, 33000),
+                                   (64, 512, 17408)])
 def test_large_outputs(M, K, n):
     """Enough rows of W that K is not split, a sample of the outputs checked (the oracle takes their rows of W alone)."""
     rng = np.random.default_rng([M, K, n])
