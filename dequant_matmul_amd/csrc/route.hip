@@ -35,7 +35,9 @@ constexpr int kSmallTokens = 8;      // one workgroup's work: 8 tokens of 256 ex
                                      // one compute unit 16 tokens take 13.1, as in two launches, 48 take 27, in two 13.5
 constexpr float kLargest = 3.4028234663852886e38f;
 
-__device__ __forceinline__ float held(float l) { return l > kLargest ? kLargest : l; }  // a NaN stays one
+// A logit as the choice takes it: +infinity is the largest number, and -0 is +0 (-0 + 0 = +0), since their order as
+// integers would tell the two zeros apart.  A NaN stays one.
+__device__ __forceinline__ float held(float l) { return l > kLargest ? kLargest : l + 0.f; }
 // The sum over the wave in fp64, the same in every lane.
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ double dpp_add_f64(double x) {

@@ -270,3 +270,19 @@ def test_refusals_of_the_binding():
             fqm.route(l, 2, out=r._replace(**{name: t}))
     with pytest.raises(ValueError, match="out.dst"):
         fqm.route(l, 2, out=r._replace(dst=None))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens,E", [(1, 4), (1, 24), (5, 24), (70, 100), (60, 256), (40, 600), (7000, 24)])
+def test_zeros_of_both_signs_are_equal(tokens, E, x, score):
+    """-0 and +0 tie as any two equal logits do: the lowest index first, whichever of them has the sign."""
+    print(f"route zeros {tokens}x{E} {x} {score}", flush=True)
+    rng = np.random.default_rng([tokens, E])
+    l = rng.choice([-1.0, -0.0, 0.0], (tokens, E))
+    l[0] = np.where(np.arange(E) % 2 == 0, -0.0, 0.0)
+    logits = torch.from_numpy(l).to(DEV, T[x])
+    assert torch.signbit(logits[0, 0]) and not torch.signbit(logits[0, 1])
+    for kw in (dict(), dict(renormalise=False), dict(bias=torch.zeros(E, device=DEV)), dict(bias=-torch.zeros(E, device=DEV)),
+               dict(groups=4, top_groups=2, group_score="max"), dict(groups=2, group_score="top2")):
+        run(logits, min(3, E // 2), score=score, **kw)
