@@ -181,6 +181,22 @@ constexpr int kStreamRows = 32;
 constexpr int kStreamWaves = 4;
 constexpr int kRing = 2;
 
+// Byte of a stage's X (16 MX rows) at which lane j of 32 finds its operand's chunk.  The matrix instruction takes 32 rows:
+// with 16, lanes 16 .. 31 read rows 0 .. 15 again, whose sums in their places are never stored.
+template <int MX>
+constexpr int stream_x_at(int j, int chunk) {
+    const int row = j & (16 * MX - 1);
+    return 256 * row + 16 * (chunk ^ (row & 15));
+}
+template <int MX>
+constexpr bool stream_x_inside() {
+    for (int j = 0; j < 32; ++j)
+        for (int chunk = 0; chunk < 16; ++chunk)
+            if (stream_x_at<MX>(j, chunk) < 0 || stream_x_at<MX>(j, chunk) + 16 > MX * 4096) return false;
+    return true;
+}
+static_assert(stream_x_inside<1>() && stream_x_inside<2>(), "every lane's operand lies in the stage's X");
+
 // Workgroup g's first stage of all tiles' `total`, and the workgroup that has stage u (32 bits hold total * groups).
 __device__ __forceinline__ uint32_t stream_first(uint32_t g, uint32_t total, uint32_t groups) { return g * total / groups; }
 __device__ __forceinline__ uint32_t stream_owner(uint32_t u, uint32_t total, uint32_t groups) {
@@ -222,10 +238,10 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
         xrow[u] = (uint32_t)min(row, M - 1) * (uint32_t)a.ld_x * 2u;
         xin[u] = 16u * ((lane & 15) ^ (row & 15));
     }
-    // operand reads: row j (+ 32), logical chunk 8 h + 4 g + q
+    // operand reads: row j, logical chunk 8 h + 4 g + q
     int aoff[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) aoff[c] = 256 * j + 16 * ((8 * (c >> 2) + 4 * g + (c & 3)) ^ (j & 15));
+    for (int c = 0; c < 8; ++c) aoff[c] = stream_x_at<MX>(j, 8 * (c >> 2) + 4 * g + (c & 3));
     // code reads of lane (j, g): its 24 (16) bytes of both steps of a stage
     constexpr int CR = BITS == 6 ? 6 : 2;
     int coff[CR];
