@@ -27,7 +27,7 @@ hipError_t launch_lut_linear_mfma(const Linear& p, bool six, float* ws, hipStrea
 namespace {
 
 // Rows of W of a run of outputs o0 .. o0 + T - 1: as they lie, or with two stacked matrices T / 2 outputs' rows of
-// the first and then the same of the second.  row(r): some row where there is none (has(r)).
+// the first and then the same of the second.  row(r): some row where there is none.
 template <int T>
 struct OutputRows {
     int n, o0, gated;

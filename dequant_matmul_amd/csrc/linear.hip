@@ -179,7 +179,6 @@ __global__ __launch_bounds__(256) void linear_reduce(const Linear p, const float
 // by row % 16.
 constexpr int kStreamRows = 32;
 constexpr int kStreamWaves = 4;
-constexpr int kRing = 2;
 
 // Byte of a stage's X (16 MX rows) at which lane j of 32 finds its operand's chunk.  The matrix instruction takes 32 rows:
 // with 16, lanes 16 .. 31 read rows 0 .. 15 again, whose sums in their places are never stored.
@@ -210,18 +209,15 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
     constexpr int MB = (MX + 1) / 2;                  // 32-row blocks of X
     constexpr int CH = BITS == 6 ? 6 : 4;             // chunks of a row's codes per stage
     constexpr int CD = CH / 2;                        // 1 KB loads of a wave's codes per stage
-    constexpr int PER = CD + MX;                      // loads of a wave per stage
     __shared__ __attribute__((aligned(8192))) uint8_t s_tab[(NW / 2) * F::PLANE];
     __shared__ __attribute__((aligned(16))) uint8_t s_zero[16];
     // objects of their own, so that the compiler sees which reads a load under way does not concern
     __shared__ __attribute__((aligned(16))) uint8_t s_c0[NW * 1024 * CD];
     __shared__ __attribute__((aligned(16))) uint8_t s_c1[NW * 1024 * CD];
-    __shared__ __attribute__((aligned(16))) uint8_t s_c2[kRing > 2 ? NW * 1024 * CD : 16];
     __shared__ __attribute__((aligned(16))) uint8_t s_x0[MX * 4096];
     __shared__ __attribute__((aligned(16))) uint8_t s_x1[MX * 4096];
-    __shared__ __attribute__((aligned(16))) uint8_t s_x2[kRing > 2 ? MX * 4096 : 16];
-    lds8* const CS[3] = {(lds8*)s_c0, (lds8*)s_c1, (lds8*)s_c2};
-    lds8* const XS[3] = {(lds8*)s_x0, (lds8*)s_x1, (lds8*)s_x2};
+    lds8* const CS[2] = {(lds8*)s_c0, (lds8*)s_c1};
+    lds8* const XS[2] = {(lds8*)s_x0, (lds8*)s_x1};
     const fqm_epilogue& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -308,7 +304,6 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
                 }
             }
             load_stage(0, s0);
-            if constexpr (kRing > 2) load_stage(1, min(s0 + 1, s1 - 1));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int v = 0; v < BN * 8 / (64 * NW); ++v) {
@@ -362,12 +357,12 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
             slice(Slice<3>{});
         };
         auto stage = [&](auto rc, int s) {
-            constexpr int R = decltype(rc)::value, R2 = (R + kRing - 1) % kRing;
+            constexpr int R = decltype(rc)::value;
             asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0x0070 | (PER * (kRing - 2)));  // vmcnt lgkmcnt(0)
+            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            load_stage(R2, min(s + kRing - 1, s1 - 1));
+            load_stage(1 - R, min(s + 1, s1 - 1));
             const bool none = 2 * s + 1 >= ksteps;  // no second half: its weights are the zero
             mask1 = none ? 0u : cmask;
             base1 = none ? (uint32_t)(uintptr_t)(lds8*)s_zero - (uint32_t)(uintptr_t)TAB : tbase;
@@ -375,13 +370,11 @@ __device__ __forceinline__ void stream_tiles(const Linear& p, int tiles, float* 
             step(rc, Slice<1>{});
         };
         int s = s0;
-        for (; s + kRing - 1 < s1; s += kRing) {
+        for (; s + 1 < s1; s += 2) {
             stage(Buf<0>{}, s);
             stage(Buf<1>{}, s + 1);
-            if constexpr (kRing > 2) stage(Buf<kRing - 1>{}, s + 2);
         }
         if (s < s1) stage(Buf<0>{}, s);
-        if constexpr (kRing > 2) if (s + 1 < s1) stage(Buf<1>{}, s + 1);
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load may still be writing this workgroup's LDS
         if (s0 == 0 && s1 == stages) {
             __syncthreads();
