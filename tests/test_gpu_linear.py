@@ -234,3 +234,93 @@ def test_refusals_of_the_binding():
     with pytest.raises(fqm.FqmError, match="workspace"):
         big, _ = weights(6, 200, 8192)
         fqm.linear(big, torch.zeros(40, 8192, dtype=torch.bfloat16, device=DEV), workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))
+
+
+# Nine to 32 rows, and fewer where no other kernel takes the width: tiles that up to 16 workgroups share through the
+# workspace, tiles of a workgroup's own between them (K 192 and 320), K of an odd number of steps.
+SHARED = [(12, 5120, 300), (16, 1024, 130), (24, 1088, 300), (32, 5120, 1000), (5, 4160, 200), (1, 704, 515), (17, 8192, 64),
+          (16, 192, 515), (31, 320, 2000)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,K,n", SHARED)
+def test_shared_tiles_on_streams_with_any_workspace_and_in_graphs(M, K, n, gated):
+    """No call reads what its workspace held before, nor does a replay."""
+    print(f"linear shared tiles M {M} {K}->{n} gated {gated}", flush=True)
+    w, _ = weights(6 if n % 8 else 4, n * (1 + gated), K)
+    x = bf16_dev(synth.activations(M, K, 5))
+    res = torch.randn(M, n, device=DEV)
+    call = lambda **kw: fqm.linear(w, x, act="silu", gated=gated, residual=res, **kw)  # noqa: E731
+    want = call(out_dtype=torch.float32)
+    need = fqm.linear_workspace_size(w, M, gated=gated, out_dtype=torch.float32)
+    assert need > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on_side = call(out_dtype=torch.float32, stream=side)
+    side.synchronize()
+    assert torch.equal(on_side, want)
+    buf, y = guarded((M, n), torch.float32)
+    for fill in (255, 127, 0):  # NaN, about 3e38, 0
+        guard = torch.full((need + 4096,), fill, dtype=torch.uint8, device=DEV)
+        y.zero_()
+        assert torch.equal(call(y=y, workspace=guard[:need]), want)
+        assert canaries_intact(buf) and (guard[need:] == fill).all()
+    ws = guard[:need]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(y=y, workspace=ws)
+    for _ in range(3):
+        x.copy_(torch.roll(x, 1, 1))
+        want = call(out_dtype=torch.float32)
+        y.zero_()
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,K,n", SHARED)
+def test_shared_tiles_in_place_of_the_residual(M, K, n, gated):
+    w, _ = weights(6 if n % 8 else 4, n * (1 + gated), K)
+    x = bf16_dev(synth.activations(M, K, 5))
+    for dt in (torch.bfloat16, torch.float32):
+        wide = torch.randn(M, n + 11, device=DEV).to(dt)
+        r = wide[:, 5:5 + n]
+        before = wide.clone()
+        want = fqm.linear(w, x, act="gelu", gated=gated, residual=r, out_dtype=dt)
+        got = fqm.linear(w, x, act="gelu", gated=gated, residual=r, y=r)
+        assert got.data_ptr() == r.data_ptr() and torch.equal(got, want)
+        assert torch.equal(wide[:, :5], before[:, :5]) and torch.equal(wide[:, 5 + n:], before[:, 5 + n:])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,K,n", [c for c in SHARED if c[0] > 1])
+def test_shared_tiles_keep_a_row_from_the_others(M, K, n, gated):
+    """All rows but one NaN and infinite: that one keeps its bits, first, last and in between."""
+    w, _ = weights(6 if n % 8 else 4, n * (1 + gated), K)
+    x = bf16_dev(synth.activations(M, K, 5))
+    want = fqm.linear(w, x, act="silu", gated=gated, out_dtype=torch.float32)
+    for m in sorted({0, 1, M // 2, M - 1}):
+        bad = torch.full_like(x, float("nan"))
+        bad[:, ::3] = float("inf")
+        bad[m] = x[m]
+        got = fqm.linear(w, bad, act="silu", gated=gated, out_dtype=torch.float32)
+        assert torch.equal(got[m], want[m])
+        assert torch.isnan(got[[i for i in range(M) if i != m]]).all()
+
+
+@pytest.mark.parametrize("M", [9, 16, 31])
+def test_two_calls_at_once_with_workspaces_of_their_own(M):
+    w, _ = weights(6, 2000, 5120)
+    x = bf16_dev(synth.activations(M, 5120, 5))
+    want = fqm.linear(w, x, act="silu", gated=True, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(8):
+        for s in streams:
+            outs.append(fqm.linear(w, x, act="silu", gated=True, out_dtype=torch.float32, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
