@@ -483,8 +483,8 @@ typedef struct fqm_epilogue {
 } fqm_epilogue;
 
 /* Bytes of device workspace fqm_linear needs on the current device (a function
- * of w's rows, cols and format and of a's M, gated and types only; a's pointers
- * may still be NULL); 0 for invalid arguments. */
+ * of w's rows, cols, format and row stride ld and of a's M, gated and types only;
+ * a's pointers may still be NULL); 0 for invalid arguments. */
 size_t fqm_linear_workspace_size(const fqm_weights* w, const fqm_epilogue* a);
 
 /* The product with everything that follows it up to the next operator:

@@ -71,6 +71,22 @@ def test_linear_formats_null_and_workspace(lib):
     assert call(FAKE + 4, need) == E["ALIGN"]
 
 
+@pytest.mark.parametrize("gated", [0, 1])
+def test_linear_workspace_goes_by_the_row_stride_as_well(stopped, gated):
+    """Rows of codes so far apart that 32-bit offsets do not reach both matrices take another kernel: the size asked for
+    the same descriptor is enough, one byte less is refused."""
+    sizes = []
+    for ld in (768, 1 << 18, 1 << 19):
+        w = lut6(rows=16384, cols=1024, ld=ld)
+        a = filled(fqm._Epilogue, dict(LINEAR, M=16, ld_x=1024, ld_y=16384, ld_res=16384, gated=gated), {})
+        need = stopped.fqm_linear_workspace_size(ctypes.byref(w), ctypes.byref(a))
+        sizes.append(need)
+        call = lambda n: stopped.fqm_linear(ctypes.byref(w), ctypes.byref(a), FAKE, n, None)  # noqa: E731
+        assert call(need) == E["BOUNDS"]
+        assert need == 0 or call(need - 1) == E["WORKSPACE"]
+    assert gated == 0 or sizes[0] != sizes[2]
+
+
 ROUTE = dict(T=9, E=24, k=3, logits=FAKE, ld_x=24, x_dtype=1, groups=4, top_groups=2, scale=1.0, expert=FAKE, weight=FAKE,
              offsets=FAKE, src=FAKE, dst=FAKE, row_scale=FAKE)
 
