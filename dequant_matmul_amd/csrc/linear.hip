@@ -10,9 +10,10 @@
 // gemv kernels with this epilogue), the stream kernel below beyond.
 //
 // What binds it, on one MI355X: the matrix cores and the tables' gathers beside them for many rows (2048 rows 5120 ->
-// 8704 gated 361 us, 1.01 PFLOP/s, of which the epilogue and the partial round's two launches are 60), the
-// weights' stream for few (1 row 17408 -> 5120 15.6 us, 4.3 TB/s of codes and tables; 16 rows 5120 -> 17408 gated
-// 42 us and 5 for the sums), launches and the parts' way through memory between (77 rows 4160 -> 1000 8.7 + 4.9 us).
+// 8704 gated 358 to 381 us on different boxes, 0.96 to 1.02 PFLOP/s, of which the epilogue and the partial round's two
+// launches are 60), the weights' stream for few (1 row 17408 -> 5120 15.6 us, 4.3 TB/s of codes and tables; 16 rows 5120 ->
+// 17408 gated 43 us and 5 for the sums), launches and the parts' way through memory between (77 rows 4160 -> 1000 9.0 +
+// 5.0 us).
 #include <algorithm>
 
 #include "linear.h"
@@ -536,11 +537,13 @@ LinearPlan tile_plan(int bm, int64_t N, int64_t K, int64_t M, bool gated) {
     return p;
 }
 
-// The height whose time should be the least.  Measured on one MI355X, us with 64 / 128 / 256 rows: 6-bit 5120 -> 17408
-// at 64 rows 37 / - / -, 96 rows 66 / 48 / 77, 128 rows 68 / 50 / 79, 192 rows 76 / 85 / 84, 256 rows 107 / 88 / 90,
-// 320 rows 113 / 99 / 139, 512 rows 168 / 148 / 152; 6-bit 5120 -> 34816 at 512 rows 304 / 238 / 197; 6-bit 17408 ->
-// 5120 at 128 rows 53 / 53 / 80, 256 rows 88 / 71 / 90, 512 rows 168 / 121 / 192; 4-bit 4160 -> 1000 at 96 rows 13.0 /
-// 14.0 / 22, 512 rows 22 / 21 / 27.
+// The height whose time should be the least.  Measured on one MI355X, us with 64 / 128 / 256 rows (no epilogue but SiLU
+// where gated, three sets of weights in turn): 6-bit 5120 -> 17408 at 64 rows 35 / - / -, 96 rows 59 / 44 / 60, 128 rows 61 /
+// 47 / -, 192 rows 68 / 82 / 65, 256 rows 100 / 88 / 68, 320 rows 105 / 94 / 124, 512 rows 165 / 142 / 133; its gated form
+// with twice the rows of W at 128 rows 114 / 95 / -, 256 rows 177 / 152 / 134, 512 rows 311 / 245 / 200; 6-bit 17408 -> 5120
+// at 128 rows 47 / 39 / -, 256 rows 85 / 68 / 67, 512 rows 161 / 123 / 106; 4-bit 4160 -> 1000 at 96 rows 12.8 / 14.0 / 22,
+// 512 rows 19.5 / 21.4 / 29.  Of these the rule takes the best or one within 5 %, but for 256 rows gated (128: 14 % more), 512
+// rows 5120 -> 17408 (128: 6 %) and 512 rows 4160 -> 1000 (128: 10 %).
 LinearPlan linear_plan(int64_t N, int64_t K, int64_t M, bool gated) {
     LinearPlan best = tile_plan(64, N, K, M, gated);
     for (const int bm : {128, 256}) {
@@ -601,9 +604,13 @@ Linear linear_of(const fqm_weights& w, const fqm_epilogue& a) {
 }
 
 // Measured: 1 row 17408 -> 5120 15.6 us on a wave a row and 31 on the tiles; 8 rows 5120 -> 17408 24 us in 16-row blocks,
-// 27 on the stream kernel; 16 rows 5120 -> 17408 gated 47 us on the stream kernel, 66 on the tiles.  Three rows, a wave
-// a row of W / 16-row blocks: 4-bit 2048 -> 4096 4.7 / 10.1, 5120 -> 17408 23.5 / 20.7, 9216 -> 17297 41 / 32 (6-bit 4.8 /
-// 10.6, 24.7 / 24.1, 44 / 39); two rows 9216 -> 17297 27 / 32 (6-bit 32 / 38).
+// 27 on the stream kernel; 16 rows 5120 -> 17408 gated 46 us on the stream kernel, 66 on the tiles.
+// Three rows, a wave a row of W / 16-row blocks, 6-bit (4-bit): below 2^26 weights the waves win, 2048 -> 4096 5.0 / 11.0 (4.6 /
+// 9.7), 5120 -> 5120 8.8 / 14.1 (8.4 / 13.1), 5120 -> 12288 17.6 / 20.2 (16.2 / 18.4); from about 10^8 on the blocks do, 12288 ->
+// 8192 30 / 25 (29 / 22), 9216 -> 17297 41 / 36 (40 / 32).  Between them it goes by how the blocks' K parts fill the card:
+// 8192 -> 8192 18.9 / 20.2 (18.2 / 18.0), 5120 -> 14336 19.4 / 22.8 (18.4 / 20.7), 12288 -> 6144 23.8 / 22.6 (23.1 / 20.3), 9216 ->
+// 8192 24.1 / 22.3 (23.3 / 19.1), 5120 -> 16384 22.6 / 19.8 (20.2 / 17.9), 5120 -> 17408 23.3 / 23.0 (21.4 / 20.1).  Two
+// rows 9216 -> 17297 27 / 32 (6-bit 32 / 38).
 enum class Path { rows, mfma, stream, tiles };
 Path path_of(const fqm_weights& w, const Linear& p) {
     const bool blocks = p.a.M <= 8 && lut_gemv_mfma_supported(w, (int)std::max<int64_t>(p.a.M, 2));

@@ -15,10 +15,11 @@
 // counter is taken by whoever comes first, so the order of a group's rows is the slots'
 // order, whatever the timing.  The fewest tokens are one workgroup's work, in one launch.
 //
-// What binds it, on one MI355X: the issue of some 780 vector and 530 scalar instructions a token (256 experts, 8
-// groups, k 8) and the waits between dependent ones, for many tokens (16384: 29 us, and 13 us for the
+// What binds it, on one MI355X: the issue of some 710 vector and 490 scalar instructions a token (256 experts, 8
+// groups, k 8) and the waits between dependent ones, for many tokens (16384: 31 us, and 13 us for the
 // plan, whose workgroups each read all tiles' counts); launches and the latency of one token's chain of steps
-// for few (1 token 5.6 us, 48 tokens 13.5 us in two launches).
+// for few (1 token 5.3 us, 48 tokens 12.6 us in two launches).  A bias of -1e4 or below on one expert opens every
+// token's choice to fp64, one at a time (16384 tokens of 256 experts, no groups, 34 -> 51 us; -infinity 33).
 #include <algorithm>
 
 #include "activation.h"

@@ -496,7 +496,8 @@ size_t fqm_linear_workspace_size(const fqm_weights* w, const fqm_epilogue* a);
  * most 2^21; w->rows at most 2^24.  Any M: single tokens and prompts.  cols == 0
  * counts as sums of nothing (v = bias).  workspace as for fqm_gemm.  Sums are
  * added in a fixed order: results do not depend on timing, nor on the other
- * rows' values.  FABQ / MDBF descriptors return FQM_E_UNSUPPORTED. */
+ * rows' values.  Y may be the residual; no other buffers may overlap.  FABQ / MDBF
+ * descriptors return FQM_E_UNSUPPORTED. */
 fqm_status fqm_linear(const fqm_weights* w, const fqm_epilogue* a, void* workspace, size_t ws_bytes, void* stream);
 
 enum fqm_score { FQM_SOFTMAX = 0, FQM_SIGMOID = 1 };
@@ -539,11 +540,14 @@ size_t fqm_route_workspace_size(const fqm_routing* a);
  *   experts  the k of them with the largest c, best first (ties: the lowest index)
  *   weight   scale * s, with renormalise scale * s / (sum of the chosen s)
  * The choice is that of exact scores (scores too near each other for fp32 are
- * formed again in fp64).  An expert is closed to a token whose logit for it is
+ * formed again in fp64); logits -0 and +0 are equal.  A weight below 2^-126 of the
+ * scale may be 0.  An expert is closed to a token whose logit for it is
  * -infinity or NaN (so is one whose bias is): it is never chosen, has no part
  * in the softmax, and a group without an open expert comes last.  A logit of
  * +infinity counts as fp32's largest number.  A token with fewer than k open
  * experts in its groups has expert -1 and weight 0 in the places that are left.
+ * A large finite bias closes an expert too, but the bound on fp32's errors grows
+ * with it, and most tokens are then formed again: -infinity costs nothing.
  * The plan lists the T * k slots (slot t k + j: token t's j-th expert) by expert,
  * a slot's number deciding within one expert, as fqm_gemm_grouped takes them:
  * offsets[e] .. offsets[e+1]-1 are expert e's rows, src their tokens, dst their
