@@ -10,7 +10,7 @@
 // gemv kernels with this epilogue), the stream kernel below beyond.
 //
 // What binds it, on one MI355X: the matrix cores and the tables' gathers beside them for many rows (2048 rows 5120 ->
-// 8704 gated 358 to 381 us on different boxes, 0.96 to 1.02 PFLOP/s, of which the epilogue and the partial round's two
+// 8704 gated 358 to 381 us by the card, 0.96 to 1.02 PFLOP/s, of which the epilogue and the partial round's two
 // launches are 60), the weights' stream for few (1 row 17408 -> 5120 15.6 us, 4.3 TB/s of codes and tables; 16 rows 5120 ->
 // 17408 gated 43 us and 5 for the sums), launches and the parts' way through memory between (77 rows 4160 -> 1000 9.0 +
 // 5.0 us).

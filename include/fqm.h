@@ -598,8 +598,9 @@ typedef struct fqm_block {
  *     y = h * (weight + weight_offset) / sqrt(mean(h^2) + eps)
  * total receives h rounded to its dtype (y is formed from the unrounded h), y
  * and y_scale as in fqm_add_rms_norm.  The means are fp32: where u or h passes
- * about 2^63 they are infinite and the norm zeros.  rows == 0 enqueues nothing;
- * cols == 0 writes zeros to y_scale. */
+ * about 2^63 they are infinite and the norm zeros; with eps == 0, squares of values
+ * below about 2^-63 lose digits and vanish (a mean of 0 makes y infinite or NaN).
+ * rows == 0 enqueues nothing; cols == 0 writes zeros to y_scale. */
 fqm_status fqm_block_norm(const fqm_block* a, void* stream);
 
 #ifdef __cplusplus
